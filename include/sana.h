@@ -300,6 +300,111 @@ SANA_API sana_status sana_softmax_anchor_sparse_fwd(const sana_shape* shape, san
                                                     sana_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions of queries and keys, and the per-head RMS norm of queries
+ * and keys with the rotation in the same pass.  (The pages give the anchors 3D
+ * RoPE and no query/key norm; these are the forms that token sequences with
+ * positions of their own, grouped heads and long contexts need: RoFormer's
+ * rotation, with the linear, NTK-aware and YaRN rescalings of its angles.)
+ *
+ * sana_rotary: a device table of (cos, sin) by position and pair, fp32
+ *   [max_positions][rotary_dim / 2][2].  Element pairs of a head:
+ *   SANA_ROTARY_INTERLEAVED (2j, 2j + 1), SANA_ROTARY_HALF (j, j +
+ *   rotary_dim / 2); elements from rotary_dim on are not rotated.
+ *   rotary_dim: a multiple of 16, at most 256 and at most head_dim.
+ * sana_rotary_table: fills such a table on the stream (angles, cosine and
+ *   sine in double).  Pair j of n = rotary_dim / 2 turns by p * f_j:
+ *     SANA_ROTARY_PLAIN   f_j = theta^(-j/n)
+ *     SANA_ROTARY_LINEAR  f_j / factor
+ *     SANA_ROTARY_NTK     theta replaced by theta * factor^(n / (n - 1))
+ *     SANA_ROTARY_YARN    (1 - g_j) f_j + g_j f_j / factor, g_j = clamp((j - lo)
+ *       / (hi - lo), 0, 1), lo = floor(d(beta_fast)), hi = ceil(d(beta_slow)),
+ *       d(b) = n ln(original / (2 pi b)) / ln(theta), lo and hi kept inside
+ *       [0, n - 1]; cosine and sine are multiplied by attention_factor
+ *       (0: 0.1 ln(factor) + 1).
+ *   scaling == NULL is SANA_ROTARY_PLAIN.  factor >= 1.
+ *
+ * sana_qk_shape: B sequences of N tokens; q (B, N, heads * head_dim), k (B, N,
+ *   kv_heads * head_dim), each token's row contiguous and tokens q_stride /
+ *   k_stride elements apart (a multiple of 8, at least the row's width; 0: the
+ *   row's width), sequences N token strides apart -- so both may be parts of
+ *   one packed projection.  kv_heads == 0: queries only, the key pointers NULL.
+ *   heads and kv_heads need not divide each other here.  head_dim 16, 32, 64,
+ *   128 or 256, bf16 or fp32.  Outputs and gradients are contiguous.
+ * sana_qk_positions: exactly one of rotary and rope.
+ *   rotary: token n of sequence b stands at offset + positions[b][n]
+ *     (positions: device int32 [B][N]) or, with positions NULL, at offset + n
+ *     (offset + N <= max_positions is checked).  A position outside the table,
+ *     which only the device sees, reads the nearest row and is reported by
+ *     sana_sync_status() as SANA_ERR_INVALID_ARG.
+ *   rope: the 3D tables of a (T, H, W) grid with T * H * W == N, frames from
+ *     `offset` on (the pair layout of the anchors; positions NULL).
+ *
+ * sana_rotary_apply:  q_out = q_mul R q, k_out = R k; inverse != 0 applies the
+ *   transposed rotation, which is the gradient of the call.
+ * sana_qk_norm_rope:  q_out = q_mul R (q_weight * q / sqrt(mean(q^2) + eps)) per
+ *   head, k_out the same without q_mul.  q_weight, k_weight: device fp32
+ *   (head_dim), NULL = ones.  Sums in fp32, one rounding at the end.
+ * sana_qk_norm_rope_bwd: given dq_out, dk_out (contiguous) and the forward's
+ *   inputs, writes dq, dk and, where the pointers are not NULL, d_q_weight,
+ *   d_k_weight (device fp32 (head_dim), summed over all rows in an order that
+ *   the shape alone fixes).  Workspace: sana_qk_norm_rope_bwd_workspace_size()
+ *   bytes, 256-byte aligned.
+ * Errors: SANA_ERR_INVALID_ARG for NULL, misaligned (16 bytes) or aliasing
+ * buffers, bad strides, sizes, positions or scaling; SANA_ERR_UNSUPPORTED for
+ * a head_dim or rotary_dim that the kernels do not cover.
+ * ------------------------------------------------------------------------- */
+typedef enum { SANA_ROTARY_INTERLEAVED = 0, SANA_ROTARY_HALF = 1 } sana_rotary_layout;
+typedef enum {
+  SANA_ROTARY_PLAIN = 0,
+  SANA_ROTARY_LINEAR = 1,
+  SANA_ROTARY_NTK = 2,
+  SANA_ROTARY_YARN = 3
+} sana_rotary_scaling_kind;
+typedef struct {
+  int kind; /* sana_rotary_scaling_kind */
+  double factor;
+  int original; /* YaRN: positions the frequencies were trained for */
+  double beta_fast, beta_slow, attention_factor;
+} sana_rotary_scaling;
+typedef struct {
+  const float* table;
+  int max_positions, rotary_dim;
+  int layout; /* sana_rotary_layout */
+} sana_rotary;
+typedef struct {
+  int B, N;
+  int heads, kv_heads, head_dim;
+  long long q_stride, k_stride;
+} sana_qk_shape;
+typedef struct {
+  const sana_rotary* rotary;
+  const sana_rope* rope;
+  int T, H, W; /* grid of rope */
+  const int* positions;
+  int offset;
+} sana_qk_positions;
+SANA_API sana_status sana_rotary_table(int max_positions, int rotary_dim, double theta,
+                                       const sana_rotary_scaling* scaling, float* table,
+                                       sana_stream_t stream);
+SANA_API sana_status sana_rotary_apply(const sana_qk_shape* shape, sana_dtype dtype,
+                                       const sana_qk_positions* at, int inverse, const void* q,
+                                       const void* k, float q_mul, void* q_out, void* k_out,
+                                       sana_stream_t stream);
+SANA_API sana_status sana_qk_norm_rope(const sana_qk_shape* shape, sana_dtype dtype,
+                                       const sana_qk_positions* at, const void* q, const void* k,
+                                       const float* q_weight, const float* k_weight, float eps,
+                                       float q_mul, void* q_out, void* k_out,
+                                       sana_stream_t stream);
+SANA_API size_t sana_qk_norm_rope_bwd_workspace_size(const sana_qk_shape* shape);
+SANA_API sana_status sana_qk_norm_rope_bwd(const sana_qk_shape* shape, sana_dtype dtype,
+                                           const sana_qk_positions* at, const void* q,
+                                           const void* k, const float* q_weight,
+                                           const float* k_weight, float eps, float q_mul,
+                                           const void* dq_out, const void* dk_out, void* dq,
+                                           void* dk, float* d_q_weight, float* d_k_weight,
+                                           void* ws, size_t ws_bytes, sana_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Block Attention Residuals router ([SV2] AttnRes equation, timestep term 0):
  *   l_i = w . v_i / sqrt(mean_c v_i^2 + rms_eps),  alpha = softmax_i(l),
  *   h = sum_i alpha_i v_i,   per token, over num_sources sources.

@@ -66,6 +66,26 @@ class StackWsLayout(Structure):
                 ("blocks", c_size_t * 16)]
 
 
+class RotaryScaling(Structure):
+    _fields_ = [("kind", c_int), ("factor", c_double), ("original", c_int), ("beta_fast", c_double),
+                ("beta_slow", c_double), ("attention_factor", c_double)]
+
+
+class RotaryStruct(Structure):
+    _fields_ = [("table", c_void_p), ("max_positions", c_int), ("rotary_dim", c_int),
+                ("layout", c_int)]
+
+
+class QkShape(Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("heads", c_int), ("kv_heads", c_int),
+                ("head_dim", c_int), ("q_stride", c_longlong), ("k_stride", c_longlong)]
+
+
+class QkPositions(Structure):
+    _fields_ = [("rotary", POINTER(RotaryStruct)), ("rope", POINTER(RopeStruct)), ("T", c_int),
+                ("H", c_int), ("W", c_int), ("positions", c_void_p), ("offset", c_int)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsana.so not built ({LIB_PATH}); run softmax_attention_sana_b200/build.py")
@@ -141,6 +161,18 @@ def _load():
         "sana_mx_linear_workspace_size": (c_size_t, [c_longlong, c_int]),
         "sana_mx_linear": (c_int, [c_longlong, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                    c_void_p, c_longlong, c_int, c_void_p, c_size_t, c_void_p]),
+        "sana_rotary_table": (c_int, [c_int, c_int, c_double, POINTER(RotaryScaling), c_void_p,
+                                      c_void_p]),
+        "sana_rotary_apply": (c_int, [POINTER(QkShape), c_int, POINTER(QkPositions), c_int, c_void_p,
+                                      c_void_p, c_float, c_void_p, c_void_p, c_void_p]),
+        "sana_qk_norm_rope": (c_int, [POINTER(QkShape), c_int, POINTER(QkPositions), c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p,
+                                      c_void_p, c_void_p]),
+        "sana_qk_norm_rope_bwd_workspace_size": (c_size_t, [POINTER(QkShape)]),
+        "sana_qk_norm_rope_bwd": (c_int, [POINTER(QkShape), c_int, POINTER(QkPositions), c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_size_t, c_void_p]),
         "sana_sync_status": (c_int, [c_void_p]),
         "sana_selftest_bounded_wait": (c_int, [ctypes.c_uint, c_void_p]),
     }
@@ -444,6 +476,173 @@ def softmax_anchor_sparse_fwd(q, k, v, gate, rope, grid, heads, keep_tiles, tile
         None if rope is None else ctypes.byref(rope.struct), scale, keep_tiles, _ptr(tiles),
         int(bool(select)), _ptr(out), _ptr(ws), ws.numel(), _stream()))
     return out, tiles
+
+
+# ---------------------------------------------------------------- rotary positions, q/k norm
+
+ROTARY_INTERLEAVED, ROTARY_HALF = 0, 1
+_LAYOUTS = {"interleaved": ROTARY_INTERLEAVED, "half": ROTARY_HALF}
+_SCALINGS = {"linear": 1, "ntk": 2, "yarn": 3}
+
+
+class Rotary:
+    """Device table of rotary (cos, sin) for positions [0, max_positions): rotary_dim elements of a
+    head are turned (the rest pass through), paired "interleaved" (2j, 2j + 1) or "half" (j, j +
+    rotary_dim / 2).  scaling: None, ("linear", factor), ("ntk", factor) or ("yarn", factor,
+    original_positions[, beta_fast, beta_slow, attention_factor]).  8 bytes a position and pair."""
+
+    def __init__(self, max_positions, rotary_dim, theta=10000.0, layout="interleaved", scaling=None,
+                 device="cuda"):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
+        sc = None
+        if scaling is not None:
+            kind, *rest = scaling
+            if kind not in _SCALINGS or not 1 <= len(rest) <= (5 if kind == "yarn" else 1) or \
+                    (kind == "yarn" and len(rest) < 2):
+                raise ValueError(f"bad rotary scaling {scaling!r}")
+            factor, original, fast, slow, att = (list(rest) + [0, 32.0, 1.0, 0.0][len(rest) - 1:])
+            sc = RotaryScaling(_SCALINGS[kind], factor, original, fast, slow, att)
+        self.max_positions, self.rotary_dim, self.layout = max_positions, rotary_dim, layout
+        self.table = torch.empty(max(max_positions, 1), max(rotary_dim // 2, 1), 2,
+                                 dtype=torch.float32, device=device)
+        with torch.cuda.device(self.table.device):
+            check(lib.sana_rotary_table(max_positions, rotary_dim, theta,
+                                        None if sc is None else ctypes.byref(sc), _ptr(self.table),
+                                        _stream()))
+        self.struct = RotaryStruct(self.table.data_ptr(), max_positions, rotary_dim, _LAYOUTS[layout])
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+
+def _token_stride(t, name, width):
+    """Elements between the tokens of a (B, N, width) tensor whose rows are contiguous and whose
+    sequences follow each other at the same stride (a slice of a packed projection is one)."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[2] != width or (width > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a CUDA tensor (B, N, {width}) with contiguous rows")
+    B, N = t.shape[:2]
+    step = t.stride(1) if N > 1 else t.stride(0) if B > 1 else width
+    if t.numel() and N > 1 and B > 1 and t.stride(0) != N * step:
+        raise ValueError(f"{name}: sequences must follow each other at the tokens' stride")
+    return step if t.numel() else width
+
+
+def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
+    """The shape and position structs of a call (and what they point to)."""
+    if q.dim() != 3 or heads < 1 or q.shape[2] % heads:
+        raise ValueError(f"q must be (B, N, heads * head_dim) with heads={heads}")
+    B, N, C = q.shape
+    D = C // heads
+    if (k is None) != (kv_heads == 0):
+        raise ValueError("k is None exactly where kv_heads is 0")
+    if k is not None and (k.dtype != q.dtype or k.shape[:2] != q.shape[:2]):
+        raise ValueError("q and k must have one dtype and the same (B, N)")
+    s = QkShape(B, N, heads, kv_heads, D, _token_stride(q, "q", C),
+                0 if k is None else _token_stride(k, "k", kv_heads * D))
+    at = QkPositions(positions=None, offset=offset)
+    if isinstance(rotary, Rope):
+        if grid is None:
+            raise ValueError("a Rope needs the tokens' grid=(T, H, W)")
+        at.rope, (at.T, at.H, at.W) = ctypes.pointer(rotary.struct), grid
+        if rotary.tables.device != q.device:
+            raise ValueError("the rotary tables are on another device than q")
+    else:
+        if grid is not None:
+            raise ValueError("grid goes with a Rope")
+        at.rotary = ctypes.pointer(rotary.struct)
+        _same_device(q, rotary.table)
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.shape != (B, N) or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 tensor (B, N)")
+        at.positions = positions.data_ptr()
+    _same_device(q, k, positions)
+    return s, at
+
+
+def _norm_weight(w, name, q, D):
+    if w is None:
+        return
+    _need(w, name)
+    if w.dtype != torch.float32 or w.shape != (D,):
+        raise ValueError(f"{name} must be fp32 ({D},)")
+    _same_device(q, w)
+
+
+def _out_like(out, name, q, width):
+    if out is None:
+        return torch.empty(*q.shape[:2], width, dtype=q.dtype, device=q.device)
+    _need(out, name)
+    if out.dtype != q.dtype or tuple(out.shape) != (*q.shape[:2], width):
+        raise ValueError(f"{name} must be {q.dtype} {(*q.shape[:2], width)}")
+    _same_device(q, out)
+    return out
+
+
+def rotary_apply(q, k, rotary, heads, kv_heads, positions=None, offset=0, grid=None, inverse=False,
+                 q_mul=1.0, q_out=None, k_out=None):
+    """(q_mul * R q, R k): the rotation of every head at its token's position -- offset + n, offset +
+    positions[b, n], or the (T, H, W) grid of a Rope.  inverse: the transposed rotation (the
+    gradient).  k is None with kv_heads 0 (then k_out is None).  bf16 or fp32."""
+    s, at = _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid)
+    q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
+    k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
+    with torch.cuda.device(q.device):
+        check(lib.sana_rotary_apply(ctypes.byref(s), _dtype_code(q), ctypes.byref(at),
+                                    int(bool(inverse)), _ptr(q), _ptr(k), q_mul, _ptr(q_out),
+                                    _ptr(k_out), _stream()))
+    return q_out, k_out
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, rotary, heads, kv_heads, positions=None, offset=0,
+                 grid=None, eps=1e-6, q_mul=1.0, q_out=None, k_out=None):
+    """RMS norm of every query and key head (weights fp32 (head_dim,), None = ones) and the rotation
+    of rotary_apply, in one pass."""
+    s, at = _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid)
+    _norm_weight(q_weight, "q_weight", q, s.head_dim)
+    _norm_weight(k_weight, "k_weight", q, s.head_dim)
+    q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
+    k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
+    with torch.cuda.device(q.device):
+        check(lib.sana_qk_norm_rope(ctypes.byref(s), _dtype_code(q), ctypes.byref(at), _ptr(q),
+                                    _ptr(k), _ptr(q_weight), _ptr(k_weight), eps, q_mul,
+                                    _ptr(q_out), _ptr(k_out), _stream()))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_size(B, N, head_dim) -> int:
+    s = QkShape(B, N, 1, 0, head_dim, 0, 0)
+    return lib.sana_qk_norm_rope_bwd_workspace_size(ctypes.byref(s))
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv_heads,
+                     positions=None, offset=0, grid=None, eps=1e-6, q_mul=1.0, ws=None):
+    """Gradients (dq, dk, d_q_weight, d_k_weight) of qk_norm_rope for its outputs' gradients; a
+    weight that is None has its gradient (that of ones) all the same, keys that are None none."""
+    s, at = _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid)
+    D = s.head_dim
+    _norm_weight(q_weight, "q_weight", q, D)
+    _norm_weight(k_weight, "k_weight", q, D)
+    dq_out = _out_like(dq_out, "dq_out", q, heads * D)
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out goes with k")
+    dk_out = None if k is None else _out_like(dk_out, "dk_out", q, kv_heads * D)
+    dq = _out_like(None, "dq", q, heads * D)
+    dk = None if k is None else _out_like(None, "dk", q, kv_heads * D)
+    dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+    dwk = None if k is None else torch.empty_like(dwq)
+    if ws is None:
+        ws = _ws(lib.sana_qk_norm_rope_bwd_workspace_size(ctypes.byref(s)), q.device)
+    _same_device(q, ws)
+    with torch.cuda.device(q.device):
+        check(lib.sana_qk_norm_rope_bwd(
+            ctypes.byref(s), _dtype_code(q), ctypes.byref(at), _ptr(q), _ptr(k), _ptr(q_weight),
+            _ptr(k_weight), eps, q_mul, _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
+            _ptr(dwk), _ptr(ws), ws.numel(), _stream()))
+    return dq, dk, dwq, dwk
 
 
 # ---------------------------------------------------------------- AttnRes, norm, GEMM

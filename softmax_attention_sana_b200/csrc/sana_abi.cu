@@ -1050,6 +1050,8 @@ sana_status sana_sync_status(sana_stream_t stream) {
   if (v != 0) {
     const int zero = 0;
     cudaMemcpy(sw, &zero, sizeof(int), cudaMemcpyHostToDevice);
+    if (v >> 16 == kDevBadPosition)
+      return fail(SANA_ERR_INVALID_ARG, "a token's position lies outside the rotary table");
     return fail(SANA_ERR_TIMEOUT, "a kernel gave up a bounded wait (code 0x%x)", v);
   }
   return SANA_OK;

@@ -17,7 +17,7 @@ namespace sana {
 // passed to kernels by address): kernels that give up a bounded wait record a
 // code there; sana_sync_status() reads and clears it.
 // ----------------------------------------------------------------------------
-enum : int { kDevOK = 0, kDevTimeout = 1 };
+enum : int { kDevOK = 0, kDevTimeout = 1, kDevBadPosition = 2 };
 
 // What a bounded wait needs: the CTA's abort flag (shared memory) and the
 // device status word.
@@ -28,6 +28,11 @@ struct WaitCtx {
 
 __device__ __forceinline__ void report_timeout(int* status, int where) {
   atomicCAS(status, 0, (kDevTimeout << 16) | (where & 0xFFFF));
+}
+
+// A token position outside the rotary table (the kernel reads the nearest row).
+__device__ __forceinline__ void report_bad_position(int* status) {
+  atomicCAS(status, 0, kDevBadPosition << 16);
 }
 
 __device__ __forceinline__ uint64_t globaltimer_ns() {

@@ -220,4 +220,36 @@ sana_status mx_gemm_run_parts(long long M, int N, int K, const void* xq, const v
                               const void* wq, const void* wsf, void* const* outs, int nparts,
                               long long ldo, int epilogue, cudaStream_t st);
 
+// ---------------------------------------------------------------- rotary positions, q/k norm
+// How a kernel finds the angles of a token: a table of (cos, sin) by position
+// (table != nullptr; position = offset + n, or offset + positions[b][n]), or
+// the 3D tables of a video grid.
+struct RotaryDev {
+  const float* table;  // [max_positions][pairs][2]
+  int pairs, max_positions;
+  bool half;           // element j pairs with j + pairs (else 2j with 2j + 1)
+  bool inverse;        // the transposed rotation
+  const int* positions;
+  int offset, N;
+  RopeDev rope;
+  GridDev grid;
+};
+// Queries and keys (or, in the gradient, dq_out / dk_out the incoming and
+// q_out / k_out the outgoing gradients).  Strides of q and k between tokens.
+struct QkTensors {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const void *dq_out, *dk_out;
+  const float *wq, *wk;
+  long long q_stride, k_stride;
+  int B, N, heads, kv_heads, head_dim;
+};
+sana_status rotary_table_run(float* table, int max_positions, int pairs, const double* inv,
+                             double mul, cudaStream_t st);
+sana_status qk_norm_rope_run(const QkTensors& a, sana_dtype dt, const RotaryDev& rt, bool norm,
+                             float eps, float q_mul, cudaStream_t st);
+size_t qk_norm_rope_bwd_ws_bytes(long long tokens, int head_dim);
+sana_status qk_norm_rope_bwd_run(const QkTensors& a, sana_dtype dt, const RotaryDev& rt, float eps,
+                                 float q_mul, float* dwq, float* dwk, void* ws, cudaStream_t st);
+
 }  // namespace sana
