@@ -405,6 +405,90 @@ SANA_API sana_status sana_qk_norm_rope_bwd(const sana_qk_shape* shape, sana_dtyp
                                            void* ws, size_t ws_bytes, sana_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Windowed softmax anchor: the gated anchor over a sliding window of the
+ * sequence and its first tokens ("sinks"), for sequences that grow ([SV1] sec.
+ * 3.4 generates block after block; the pages' anchors see the whole clip, so
+ * the window is this library's).  No rotation inside: q and k come from
+ * sana_qk_norm_rope or sana_rotary_apply.
+ *
+ * The N queries are the last N of N_keys positions.  A query at position p
+ * sees key j iff j < min(e, length) and (j >= e - window or j < sinks), where
+ * e = (p / block + 1) * block is the end of p's own block of `block` positions
+ * (block = 1: causal; block = frames * tokens of a frame: block-causal video).
+ *   Y = sigmoid(G) * softmax(scale Q K^T over the visible keys) V,
+ * query head h reading key head h / (heads / kv_heads).
+ * sana_window_shape:
+ *   q (B, N, heads, 128), k and v (B, N_keys, kv_heads, 128), gate_logits like
+ *   q or NULL, bf16; each token's row contiguous, tokens *_stride elements apart
+ *   (a multiple of 8, at least the row's width; 0: the row's width), sequences
+ *   N (N_keys) token strides apart.  heads a multiple of kv_heads.
+ *   window: 0 = no limit, else at least block.  sinks >= 0.  block >= 1.  All
+ *   of N_keys, window, sinks and block at most 2^30.
+ *   lengths: device int32 [B] or NULL: tokens of each sequence (values outside
+ *   [0, N_keys] count as the nearest of them).  Padding from there on sees
+ *   nothing and is seen by nothing, whatever its rows hold: zeros are written
+ *   for it, also in the gradients.
+ *   scale <= 0 selects 1/sqrt(128).
+ * sana_window_anchor_fwd: out (B, N, heads, 128) contiguous; lse (device fp32
+ *   [B][heads][N], natural logarithm; -inf for a row that sees nothing) or NULL.
+ * sana_window_anchor_bwd: given the forward's out and lse and dy (contiguous),
+ *   writes dq (B, N, heads, 128), dk, dv (B, N_keys, kv_heads, 128) and, with a
+ *   gate, d_gate, all contiguous.  Deterministic: every sum runs in an order
+ *   that the shape fixes.  Workspace: sana_window_anchor_bwd_workspace_size()
+ *   bytes (gated != 0 for a call with a gate), 256-byte aligned.
+ * Accuracy: scores and sums in fp32; P, dS and sigmoid(G) dy are rounded to
+ * bf16 as operands of the next product.  A non-finite value in a real token's
+ * row can reach the rows that share a 128-key tile with it.
+ *
+ * sana_window_anchor_decode: the N newest tokens (N small, usually 1) of every
+ *   sequence over a cache of sinks and window that does not grow.  q (B, N,
+ *   heads, 128), k_new, v_new (B, N, kv_heads, 128), contiguous.  k_cache, v_cache
+ *   (B, capacity, kv_heads, 128), contiguous: position p lives in slot p while p
+ *   < capacity and in slot sinks + (p - sinks) % (capacity - sinks) after, so a
+ *   cache that is never filled is an ordinary one.  lengths: device int32 [B],
+ *   tokens that each cache already holds; the new tokens take the positions
+ *   lengths[b] ... lengths[b] + N - 1.  The call writes them into the caches and
+ *   attends (block = 1); it does not change lengths.  Positions that the ring
+ *   has overwritten are not visible, also to the first of the N tokens.  A
+ *   negative length is an empty batch entry: nothing is appended, zeros come
+ *   out.  capacity >= sinks + N.  Workspace:
+ *   sana_window_anchor_decode_workspace_size() bytes, 256-byte aligned.
+ * Errors: SANA_ERR_INVALID_ARG for NULL, misaligned (16 bytes) or aliasing
+ * buffers and bad sizes or strides; SANA_ERR_UNSUPPORTED for a head_dim other
+ * than 128 and sizes past the limits.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int B, N, N_keys;
+  int heads, kv_heads, head_dim;
+  long long q_stride, k_stride, v_stride, gate_stride;
+  int window, sinks, block;
+  const int* lengths;
+  float scale;
+} sana_window_shape;
+SANA_API sana_status sana_window_anchor_fwd(const sana_window_shape* shape, const void* q,
+                                            const void* k, const void* v, const void* gate_logits,
+                                            void* out, float* lse, sana_stream_t stream);
+SANA_API size_t sana_window_anchor_bwd_workspace_size(const sana_window_shape* shape, int gated);
+SANA_API sana_status sana_window_anchor_bwd(const sana_window_shape* shape, const void* q,
+                                            const void* k, const void* v, const void* gate_logits,
+                                            const void* out, const float* lse, const void* dy,
+                                            void* dq, void* dk, void* dv, void* d_gate, void* ws,
+                                            size_t ws_bytes, sana_stream_t stream);
+typedef struct {
+  int B, N;
+  int heads, kv_heads, head_dim;
+  int capacity, window, sinks;
+  float scale;
+} sana_window_decode_shape;
+SANA_API size_t sana_window_anchor_decode_workspace_size(const sana_window_decode_shape* shape);
+SANA_API sana_status sana_window_anchor_decode(const sana_window_decode_shape* shape,
+                                               const void* q, const void* k_new,
+                                               const void* v_new, const void* gate_logits,
+                                               void* k_cache, void* v_cache, const int* lengths,
+                                               void* out, void* ws, size_t ws_bytes,
+                                               sana_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Block Attention Residuals router ([SV2] AttnRes equation, timestep term 0):
  *   l_i = w . v_i / sqrt(mean_c v_i^2 + rms_eps),  alpha = softmax_i(l),
  *   h = sum_i alpha_i v_i,   per token, over num_sources sources.

@@ -16,7 +16,8 @@ from ._lib import (EPI_NONE, EPI_RESIDUAL, EPI_SILU, Rope, Rotary, SanaError, at
                    softmax_anchor_rotated_fwd,
                    anchor_tile_count, softmax_anchor_fwd, softmax_anchor_sparse_fwd,
                    softmax_anchor_sparse_workspace_size, stack_config,
-                   sync_status)
+                   sync_status, window_anchor_bwd, window_anchor_bwd_workspace_size,
+                   window_anchor_decode, window_anchor_decode_workspace_size, window_anchor_fwd)
 
 __all__ = [
     "EPI_NONE", "EPI_RESIDUAL", "EPI_SILU", "Rope", "Rotary", "SanaError", "attnres_route",
@@ -30,5 +31,6 @@ __all__ = [
     "softmax_anchor_rotated_fwd",
     "anchor_tile_count", "softmax_anchor_fwd", "softmax_anchor_sparse_fwd",
     "softmax_anchor_sparse_workspace_size", "stack_config",
-    "sync_status",
+    "sync_status", "window_anchor_bwd", "window_anchor_bwd_workspace_size",
+    "window_anchor_decode", "window_anchor_decode_workspace_size", "window_anchor_fwd",
 ]

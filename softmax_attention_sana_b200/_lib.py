@@ -86,6 +86,19 @@ class QkPositions(Structure):
                 ("H", c_int), ("W", c_int), ("positions", c_void_p), ("offset", c_int)]
 
 
+class WindowShape(Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("N_keys", c_int), ("heads", c_int), ("kv_heads", c_int),
+                ("head_dim", c_int), ("q_stride", c_longlong), ("k_stride", c_longlong),
+                ("v_stride", c_longlong), ("gate_stride", c_longlong), ("window", c_int),
+                ("sinks", c_int), ("block", c_int), ("lengths", c_void_p), ("scale", c_float)]
+
+
+class WindowDecodeShape(Structure):
+    _fields_ = [("B", c_int), ("N", c_int), ("heads", c_int), ("kv_heads", c_int),
+                ("head_dim", c_int), ("capacity", c_int), ("window", c_int), ("sinks", c_int),
+                ("scale", c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libsana.so not built ({LIB_PATH}); run softmax_attention_sana_b200/build.py")
@@ -173,6 +186,14 @@ def _load():
                                           c_void_p, c_void_p, c_void_p, c_float, c_float, c_void_p,
                                           c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                           c_void_p, c_size_t, c_void_p]),
+        "sana_window_anchor_fwd": (c_int, [POINTER(WindowShape), c_void_p, c_void_p, c_void_p,
+                                           c_void_p, c_void_p, c_void_p, c_void_p]),
+        "sana_window_anchor_bwd_workspace_size": (c_size_t, [POINTER(WindowShape), c_int]),
+        "sana_window_anchor_bwd": (c_int, [POINTER(WindowShape)] + [c_void_p] * 12 + [c_size_t,
+                                                                                      c_void_p]),
+        "sana_window_anchor_decode_workspace_size": (c_size_t, [POINTER(WindowDecodeShape)]),
+        "sana_window_anchor_decode": (c_int, [POINTER(WindowDecodeShape)] + [c_void_p] * 9 +
+                                      [c_size_t, c_void_p]),
         "sana_sync_status": (c_int, [c_void_p]),
         "sana_selftest_bounded_wait": (c_int, [ctypes.c_uint, c_void_p]),
     }
@@ -643,6 +664,125 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv
             _ptr(k_weight), eps, q_mul, _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
             _ptr(dwk), _ptr(ws), ws.numel(), _stream()))
     return dq, dk, dwq, dwk
+
+
+# ---------------------------------------------------------------- windowed anchor
+
+def _window_shape(q, k, v, gate, heads, kv_heads, window, sinks, block, lengths, scale):
+    """The shape struct of a call on q, gate (B, N, heads * 128) and k, v (B, N_keys, kv_heads * 128)."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (gate, "gate")):
+        if t is not None and t.dtype != torch.bfloat16:
+            raise TypeError(f"{n} must be bfloat16")
+    if q.dim() != 3 or k.dim() != 3 or heads < 1 or q.shape[2] % heads:
+        raise ValueError(f"q must be (B, N, heads * head_dim) with heads={heads}, k (B, N_keys, ...)")
+    B, N, C = q.shape
+    D = C // heads
+    Nk = k.shape[1]
+    if k.shape[0] != B or v.shape[:2] != k.shape[:2]:
+        raise ValueError("q, k and v must have one batch size, k and v one length")
+    if gate is not None and gate.shape != q.shape:
+        raise ValueError("gate must have q's shape")
+    ld = [_token_stride(t, n, w) for t, n, w in ((q, "q", C), (k, "k", kv_heads * D), (v, "v", kv_heads * D))]
+    ld.append(0 if gate is None else _token_stride(gate, "gate", C))
+    if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,) or
+                                not lengths.is_contiguous()):
+        raise ValueError("lengths must be a contiguous int32 tensor (B,)")
+    _same_device(q, k, v, gate, lengths)
+    return WindowShape(B, N, Nk, heads, kv_heads, D, *ld, window, sinks, block,
+                       None if lengths is None else lengths.data_ptr(), scale)
+
+
+def window_anchor_fwd(q, k, v, gate, heads, kv_heads, window, sinks=0, block=1, lengths=None,
+                      scale=0.0, out=None, lse=None, want_lse=False):
+    """Gated softmax attention over a sliding window and the first `sinks` tokens (bf16, head_dim
+    128; rotate q and k first).  The N queries are the last of k's N_keys positions; one at position
+    p sees key j iff j < min(e, length) and (j >= e - window or j < sinks), e = (p // block + 1) *
+    block; window 0: no limit.  gate may be None, lengths (B,) int32 or None.  Returns out, or (out,
+    lse) with lse (B, heads, N) fp32."""
+    s = _window_shape(q, k, v, gate, heads, kv_heads, window, sinks, block, lengths, scale)
+    out = _out_like(out, "out", q, q.shape[2])
+    if lse is None and want_lse:
+        lse = torch.empty(s.B, heads, s.N, dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse")
+        _same_device(q, lse)
+        if lse.dtype != torch.float32 or lse.shape != (s.B, heads, s.N):
+            raise ValueError("lse must be fp32 (B, heads, N)")
+    with torch.cuda.device(q.device):
+        check(lib.sana_window_anchor_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate),
+                                         _ptr(out), _ptr(lse), _stream()))
+    return out if lse is None else (out, lse)
+
+
+def window_anchor_bwd_workspace_size(B, N, N_keys, heads, kv_heads, window, sinks=0, block=1,
+                                     gated=False, head_dim=128) -> int:
+    s = WindowShape(B, N, N_keys, heads, kv_heads, head_dim, 0, 0, 0, 0, window, sinks, block, None, 0.0)
+    return lib.sana_window_anchor_bwd_workspace_size(ctypes.byref(s), int(bool(gated)))
+
+
+def window_anchor_bwd(q, k, v, gate, out, lse, dy, heads, kv_heads, window, sinks=0, block=1,
+                      lengths=None, scale=0.0, ws=None):
+    """Gradients (dq, dk, dv, dgate) of window_anchor_fwd for dY, given its inputs, out and lse
+    (dgate is None without a gate)."""
+    s = _window_shape(q, k, v, gate, heads, kv_heads, window, sinks, block, lengths, scale)
+    out, dy = _out_like(out, "out", q, q.shape[2]), _out_like(dy, "dy", q, q.shape[2])
+    _need(lse, "lse")
+    _same_device(q, lse)
+    if lse.dtype != torch.float32 or lse.shape != (s.B, heads, s.N):
+        raise ValueError("lse must be fp32 (B, heads, N)")
+    dq = _out_like(None, "dq", q, q.shape[2])
+    dk, dv = _out_like(None, "dk", k, k.shape[2]), _out_like(None, "dv", v, v.shape[2])
+    dg = None if gate is None else _out_like(None, "dgate", q, q.shape[2])
+    if s.N == 0:  # no queries: nothing reaches the keys
+        return dq, dk.zero_(), dv.zero_(), dg
+    if ws is None:
+        ws = _ws(lib.sana_window_anchor_bwd_workspace_size(ctypes.byref(s), int(gate is not None)), q.device)
+    _same_device(q, ws)
+    with torch.cuda.device(q.device):
+        check(lib.sana_window_anchor_bwd(
+            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out), _ptr(lse), _ptr(dy),
+            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ws), ws.numel(), _stream()))
+    return dq, dk, dv, dg
+
+
+def window_anchor_decode_workspace_size(B, N, heads, kv_heads, capacity, window, sinks=0,
+                                        head_dim=128) -> int:
+    s = WindowDecodeShape(B, N, heads, kv_heads, head_dim, capacity, window, sinks, 0.0)
+    return lib.sana_window_anchor_decode_workspace_size(ctypes.byref(s))
+
+
+def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_heads, window, sinks=0,
+                         scale=0.0, out=None, ws=None):
+    """One step of the N newest tokens of every sequence: writes k, v (B, N, kv_heads * 128) into the
+    ring caches (B, capacity, kv_heads * 128) at positions lengths[b] + n and attends over the sinks
+    and the window (bf16).  Position p lives in slot p while p < capacity, then in slot sinks + (p -
+    sinks) % (capacity - sinks).  lengths (B,) int32 is left as it is; a negative one is an empty
+    batch entry (nothing written, zeros out)."""
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (gate, "gate"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t is not None:
+            _need(t, n)
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{n} must be bfloat16")
+    if q.dim() != 3 or k_cache.dim() != 3 or heads < 1 or q.shape[2] % heads:
+        raise ValueError(f"q must be (B, N, heads * head_dim) with heads={heads}, caches (B, capacity, ...)")
+    B, N, C = q.shape
+    D = C // heads
+    if k.shape != (B, N, kv_heads * D) or v.shape != k.shape or (gate is not None and gate.shape != q.shape):
+        raise ValueError("k and v must be (B, N, kv_heads * head_dim), gate like q")
+    if k_cache.shape != (B, k_cache.shape[1], kv_heads * D) or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must be (B, capacity, kv_heads * head_dim)")
+    if lengths.dtype != torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
+        raise ValueError("lengths must be a contiguous int32 tensor (B,)")
+    _same_device(q, k, v, gate, k_cache, v_cache, lengths, ws)
+    s = WindowDecodeShape(B, N, heads, kv_heads, D, k_cache.shape[1], window, sinks, scale)
+    out = _out_like(out, "out", q, C)
+    if ws is None:
+        ws = _ws(lib.sana_window_anchor_decode_workspace_size(ctypes.byref(s)), q.device)
+    with torch.cuda.device(q.device):
+        check(lib.sana_window_anchor_decode(
+            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(k_cache), _ptr(v_cache),
+            _ptr(lengths), _ptr(out), _ptr(ws), ws.numel(), _stream()))
+    return out
 
 
 # ---------------------------------------------------------------- AttnRes, norm, GEMM

@@ -28,7 +28,8 @@ unsigned long long current_context_id();
 // gives the device a new context), under a lock, so no launch of that family
 // runs before its attributes are set.
 enum AttrKey : int {
-  kAttrLinattn = 0, kAttrLinattnBwd, kAttrAnchor, kAttrGemm, kAttrMx128, kAttrMx256, kAttrKeys
+  kAttrLinattn = 0, kAttrLinattnBwd, kAttrAnchor, kAttrGemm, kAttrMx128, kAttrMx256, kAttrWindowFwd,
+  kAttrWindowBwd, kAttrKeys
 };
 void once_per_context(int key, void (*set)());
 // Device address of the status word of the current device.
@@ -251,5 +252,29 @@ sana_status qk_norm_rope_run(const QkTensors& a, sana_dtype dt, const RotaryDev&
 size_t qk_norm_rope_bwd_ws_bytes(long long tokens, int head_dim);
 sana_status qk_norm_rope_bwd_run(const QkTensors& a, sana_dtype dt, const RotaryDev& rt, float eps,
                                  float q_mul, float* dwq, float* dwk, void* ws, cudaStream_t st);
+
+// ---------------------------------------------------------------- windowed anchor
+// Strides in elements between tokens; scale > 0; window 0 = no limit.
+struct WindowCall {
+  const void *q, *k, *v, *gate;
+  long long q_stride, k_stride, v_stride, gate_stride;
+  int B, N, N_keys, heads, kv_heads;
+  int window, sinks, block;
+  const int* lengths;
+  float scale;
+};
+sana_status window_fwd_run(const WindowCall& c, float* lse, void* out, cudaStream_t st);
+size_t window_bwd_ws_bytes(const WindowCall& c);
+sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse, const void* dy,
+                           void* dq, void* dk, void* dv, void* dg, void* ws, cudaStream_t st);
+
+struct DecodeCall {
+  int B, N, heads, kv_heads, capacity, window, sinks;
+  float scale;
+};
+size_t window_decode_ws_bytes(const DecodeCall& c);
+sana_status window_decode_run(const DecodeCall& c, const void* q, const void* k_new,
+                              const void* v_new, const void* gate, void* k_cache, void* v_cache,
+                              const int* lengths, void* out, void* ws, cudaStream_t st);
 
 }  // namespace sana

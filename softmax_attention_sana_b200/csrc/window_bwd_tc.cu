@@ -1,0 +1,830 @@
+// Windowed softmax anchor, backward, bf16 on tcgen05 (the mask: window.cuh).
+//
+// With s_ij = scale q_i . k_j, p_ij = exp(s_ij - lse_i), o_i = sum_j p_ij v_j and
+// y_i = sigmoid(g_i) o_i, for dy:
+//   do = sigmoid(g) dy,  dg = dy y (1 - sigmoid(g)),  delta_i = dy_i . y_i (= do_i . o_i)
+//   ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i,
+// dk and dv summed over the query heads that share the key head.
+//
+// Four kernels; every sum runs in an order that the shape alone fixes:
+//   prep   row statistics (-lse log2 e, -delta), and with a gate do and dg (HBM)
+//   dkv    one CTA per (key tile, key head, batch, share of its query tiles):
+//          scores transposed (thread = key), S^T = K Q^T and dP^T = V dO^T, then
+//          dV += P^T dO and dK += dS^T Q with P^T and dS^T from TMEM
+//   join   sums the shares of key tiles that were split (few key tiles, or the
+//          sinks, which every later query sees)
+//   dq     one CTA per (query tile, query head, batch): S and dP once more, then
+//          dQ += dS K.
+// Making S and dP twice costs 7 products instead of 5, and keeps dQ out of
+// memory until it is whole: the other way round it would be added up in fp32
+// over the key tiles, 64 KB through L2 for every tile pair, in an order to be
+// enforced.
+//
+// dkv and dq share one plan: a 128 x 128 tile pair is done in two halves of 64
+// columns, each with its own softmax warpgroup and its own S and dP columns in
+// TMEM, so the tensor core works for one half while the other's exponentials
+// run.  P and dS go over the S columns, so a half's dP columns are free as soon
+// as dS is written: the next dP product is issued there at once and covers the
+// wait for the products that still read P and dS.
+#include <cuda.h>
+
+#include "f32x2.cuh"
+#include "sana_internal.h"
+#include "window.cuh"
+
+namespace sana {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kRows = kWinTile;
+constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
+constexpr int kTileB = 2 * kHalf;      // 32 KB
+constexpr int kStages = 2;
+constexpr int kThreads = 320;          // 8 softmax warps + producer + MMA
+constexpr int kWarpProd = 8, kWarpMma = 9;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// ---------------------------------------------------------------- prep
+// A half-warp per (batch, row, head); rows [N, N_pad) only get their statistics.
+template <bool kGate>
+__global__ void __launch_bounds__(256)
+    window_prep_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16* __restrict__ dy,
+                       const __nv_bfloat16* __restrict__ gate, long long gate_stride,
+                       const float* __restrict__ lse, const WindowDev w, int B, int n_pad,
+                       float* __restrict__ nlse, float* __restrict__ ndelta,
+                       __nv_bfloat16* __restrict__ d_o, __nv_bfloat16* __restrict__ dg) {
+  const int sub = threadIdx.x & 15;
+  const long long id = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const long long rows = (long long)B * n_pad * w.heads;
+  // whole half-warps past the end have nothing to do, but take part in the shuffles
+  const bool in = id < rows;
+  const int h = in ? (int)(id % w.heads) : 0;
+  const long long bn = in ? id / w.heads : 0;
+  const int b = (int)(bn / n_pad), n = (int)(bn % n_pad);
+  const bool real = in && n < w.N;
+  const bool live = real && w.off + n < window_length(w, b);
+  const size_t tok = (size_t)b * w.N + n;
+  const size_t at = (tok * w.heads + h) * kD + sub * 8;
+  float sum = 0.f;
+  uint32_t dow[4] = {0, 0, 0, 0}, dgw[4] = {0, 0, 0, 0};
+  if (live) {
+    const uint4 yv = __ldcs(reinterpret_cast<const uint4*>(y + at));
+    const uint4 dv = __ldcs(reinterpret_cast<const uint4*>(dy + at));
+    const uint32_t ya[4] = {yv.x, yv.y, yv.z, yv.w}, da[4] = {dv.x, dv.y, dv.z, dv.w};
+    uint32_t ga[4] = {0, 0, 0, 0};
+    if (kGate) {
+      const uint4 gv = __ldcs(reinterpret_cast<const uint4*>(gate + tok * gate_stride + (size_t)h * kD + sub * 8));
+      ga[0] = gv.x; ga[1] = gv.y; ga[2] = gv.z; ga[3] = gv.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = bf2_to_f2(ya[i]), d = bf2_to_f2(da[i]);
+      const float t0 = a.x * d.x, t1 = a.y * d.y;
+      sum += t0 + t1;
+      if (kGate) {
+        const float2 g = bf2_to_f2(ga[i]);
+        dow[i] = f2_to_bf2(d.x * sigmoid_fast(g.x), d.y * sigmoid_fast(g.y));
+        dgw[i] = f2_to_bf2(t0 * sigmoid_fast(-g.x), t1 * sigmoid_fast(-g.y));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  if (kGate && real) {
+    *reinterpret_cast<uint4*>(d_o + at) = make_uint4(dow[0], dow[1], dow[2], dow[3]);
+    __stcs(reinterpret_cast<uint4*>(dg + at), make_uint4(dgw[0], dgw[1], dgw[2], dgw[3]));
+  }
+  if (in && sub == 0) {
+    const size_t row = (size_t)b * w.heads + h;
+    // a row that sees nothing has lse = -inf; its terms are 2^-inf here
+    const float l = live ? lse[row * w.N + n] : -INFINITY;
+    nlse[row * n_pad + n] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+    ndelta[row * n_pad + n] = live ? -sum : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------- dkv
+// Positions of the queries that see key j: [first, last).
+__device__ __forceinline__ int key_first(const WindowDev& w, int j) {
+  return w.block == 1 ? j : j / w.block * w.block;
+}
+__device__ __forceinline__ int key_last(const WindowDev& w, int j) {
+  if (w.window == 0 || j < w.sinks) return 0x7fffffff;
+  return w.block == 1 ? j + w.window : (j + w.window) / w.block * w.block;
+}
+
+// Query tiles (of rows) that see some key of tile kt: [first, first + count).
+struct QSpan {
+  int first, count;
+};
+__device__ __forceinline__ QSpan query_span(const WindowDev& w, int kt, int len) {
+  const int j0 = kt * kWinTile, j1 = min(j0 + kWinTile, len) - 1;
+  QSpan s{0, 0};
+  if (j1 < j0) return s;
+  const int a = max(key_first(w, j0), w.off);
+  int z = min(w.off + w.N, len);
+  z = min(z, j0 < w.sinks ? 0x7fffffff : key_last(w, j1));
+  if (a >= z) return s;
+  s.first = (a - w.off) / kRows;
+  s.count = (z - 1 - w.off) / kRows - s.first + 1;
+  return s;
+}
+
+// How the host cut the work: key tiles [0, sink_tiles) into sink_parts shares
+// each, the others into win_parts, of `chunk` (query head, query tile) steps.
+struct DkvPlan {
+  int tiles, sink_tiles, sink_parts, win_parts, chunk;
+};
+
+struct DkvCtl {
+  uint64_t kv_full;
+  uint64_t q_full[kStages], q_empty[kStages];
+  uint64_t s_full[2], p_full[2], ds_full[2], mm_done[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const WindowDev w, const DkvPlan plan, float sl, float scale, int n_pad,
+                      const float* __restrict__ nlse, const float* __restrict__ ndelta,
+                      float* __restrict__ part, __nv_bfloat16* __restrict__ dk,
+                      __nv_bfloat16* __restrict__ dv, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ DkvCtl ctl;
+  __shared__ __align__(16) float stat[kStages][2][kRows];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* k_s = smem;
+  uint8_t* v_s = k_s + kTileB;
+  uint8_t* q_s = v_s + kTileB;              // ring of query tiles
+  uint8_t* do_s = q_s + kStages * kTileB;   // ring of their do tiles
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.y, b = blockIdx.z, group = w.heads / w.kv_heads;
+  int kt, share, parts;
+  {
+    const int x = blockIdx.x, in_sinks = plan.sink_tiles * plan.sink_parts;
+    if (x < in_sinks) {
+      parts = plan.sink_parts;
+      kt = x / parts;
+      share = x - kt * parts;
+    } else {
+      parts = plan.win_parts;
+      kt = (x - in_sinks) / parts;
+      share = x - in_sinks - kt * parts;
+      kt += plan.sink_tiles;
+    }
+  }
+  const int len = window_length(w, b);
+  const QSpan qs = query_span(w, kt, len);
+  const int step0 = share * plan.chunk;
+  const int steps = max(0, min(group * qs.count - step0, plan.chunk));
+  const WaitCtx wc{&ctl.abort_flag, status};
+  auto head_of = [&](int t) { return hk * group + (step0 + t) / qs.count; };
+  auto qrow_of = [&](int t) { return (qs.first + (step0 + t) % qs.count) * kRows; };
+
+  if (tid == 0) {
+    mbar_init(&ctl.kv_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl.q_full[i], 1);
+      mbar_init(&ctl.q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 128);
+      mbar_init(&ctl.ds_full[i], 128);
+      mbar_init(&ctl.mm_done[i], 1);
+    }
+    ctl.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  // columns: S^T halves [0,64) [64,128), dP^T halves [128,192) [192,256), dV, dK
+  const uint32_t t_dv = tmem + 256, t_dk = tmem + 384;
+
+  if (warp == kWarpProd) {
+    if (lane == 0 && steps > 0) {
+      mbar_arrive_expect_tx(&ctl.kv_full, 2 * kTileB);
+      tma_load_3d(k_s, &tm_k, &ctl.kv_full, hk * kD, kt * kRows, b);
+      tma_load_3d(k_s + kHalf, &tm_k, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
+      tma_load_3d(v_s, &tm_v, &ctl.kv_full, hk * kD, kt * kRows, b);
+      tma_load_3d(v_s + kHalf, &tm_v, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
+      int n = 0;
+      for (int t = 0; t < steps; ++t) {
+        const int st = t % kStages, h = head_of(t), row = qrow_of(t);
+        if (t >= kStages && !mbar_wait(&ctl.q_empty[st], ((t / kStages) - 1) & 1, wc, 0xa1)) break;
+        mbar_arrive_expect_tx(&ctl.q_full[st], 2 * kTileB + 2 * kRows * 4);
+        tma_load_3d(q_s + st * kTileB, &tm_q, &ctl.q_full[st], h * kD, row, b);
+        tma_load_3d(q_s + st * kTileB + kHalf, &tm_q, &ctl.q_full[st], h * kD + 64, row, b);
+        tma_load_3d(do_s + st * kTileB, &tm_do, &ctl.q_full[st], h * kD, row, b);
+        tma_load_3d(do_s + st * kTileB + kHalf, &tm_do, &ctl.q_full[st], h * kD + 64, row, b);
+        const size_t at = ((size_t)b * w.heads + h) * n_pad + row;
+        bulk_load(stat[st][0], nlse + at, kRows * 4, &ctl.q_full[st]);
+        bulk_load(stat[st][1], ndelta + at, kRows * 4, &ctl.q_full[st]);
+        ++n;
+      }
+      if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
+        mbar_drain(&ctl.kv_full, 0);
+        for (int t = n > kStages ? n - kStages : 0; t < n; ++t) mbar_drain(&ctl.q_full[t % kStages], (t / kStages) & 1);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0 && steps > 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, 64, 0, 0);   // K Q_w^T, V dO_w^T
+      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // P^T dO_w, dS^T Q_w (rows of B along K)
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), 16, 1024);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t dd0 = smem_desc_sw128(smem_u32(do_s), 16, 1024);
+      const uint64_t mq0 = smem_desc_sw128(smem_u32(q_s), kHalf, 1024);
+      const uint64_t md0 = smem_desc_sw128(smem_u32(do_s), kHalf, 1024);
+      // D (128 x 64) = A B_w^T over the 64 rows of half w
+      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bq, int w2) {
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_ss(d, desc_advance(a, o), desc_advance(bq, o + w2 * 8192), idesc_s, kk != 0);
+        }
+      };
+      // D (128 x 128) += A_w (TMEM) B over the 64 rows of half w
+      auto issue_acc = [&](uint32_t d, uint32_t a, uint64_t bm, int w2, bool acc) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts(d, a + kk * 8, desc_advance(bm, w2 * 8192 + kk * 2048), idesc_g, acc || kk != 0);
+      };
+      bool ok = mbar_wait(&ctl.kv_full, 0, wc, 0xa2) && mbar_wait(&ctl.q_full[0], 0, wc, 0xa3);
+      if (ok) {
+        tc_fence_after();
+        for (int i = 0; i < 2; ++i) {
+          issue_ab(tmem + 128 + i * 64, dv0, dd0, i);
+          issue_ab(tmem + i * 64, dk0, dq0, i);
+          umma_commit(&ctl.s_full[i]);
+        }
+      }
+      for (int t = 0; ok && t < steps; ++t) {
+        const uint32_t cur = (t % kStages) * kTileB, nxt = ((t + 1) % kStages) * kTileB;
+        for (int i = 0; i < 2; ++i) {
+          ok = mbar_wait(&ctl.p_full[i], t & 1, wc, 0xa4);
+          if (!ok) break;
+          tc_fence_after();
+          issue_acc(t_dv, tmem + i * 64, desc_advance(md0, cur), i, t > 0 || i > 0);
+          ok = mbar_wait(&ctl.ds_full[i], t & 1, wc, 0xa5);
+          if (!ok) break;
+          tc_fence_after();
+          issue_acc(t_dk, tmem + i * 64 + 32, desc_advance(mq0, cur), i, t > 0 || i > 0);
+          umma_commit(&ctl.mm_done[i]);
+          if (i == 1) umma_commit(&ctl.q_empty[t % kStages]);
+          if (t + 1 < steps) {
+            if (i == 0) ok = mbar_wait(&ctl.q_full[(t + 1) % kStages], ((t + 1) / kStages) & 1, wc, 0xa3);
+            if (!ok) break;
+            tc_fence_after();
+            issue_ab(tmem + 128 + i * 64, dv0, desc_advance(dd0, nxt), i);
+            // the products that read P and dS of this half have finished
+            ok = mbar_wait(&ctl.mm_done[i], t & 1, wc, 0xa6);
+            if (!ok) break;
+            tc_fence_after();
+            issue_ab(tmem + i * 64, dk0, desc_advance(dq0, nxt), i);
+            umma_commit(&ctl.s_full[i]);
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax warps: thread = key row
+    const int hf = warp >> 2;              // which half of the query tile
+    const int r = (warp & 3) * 32 + lane;  // key row
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + hf * 64 + lane_base, t_dp = tmem + 128 + hf * 64 + lane_base;
+    const int j0 = kt * kRows, j = j0 + r;
+    const int q_end = min(w.off + w.N, len);
+    const int first = key_first(w, j), last = j < len ? min(key_last(w, j), q_end) : 0;
+    const int all_first = key_first(w, j0 + kRows - 1);
+    const int all_last = j0 + kRows <= len ? min(j0 + kRows <= w.sinks ? 0x7fffffff : key_last(w, max(j0, w.sinks)), q_end) : 0;
+    const uint64_t sl2 = pk2(sl, sl);
+    bool ok = true;
+    for (int t = 0; t < steps; ++t) {
+      const int st = t % kStages;
+      const int row = qrow_of(t) + hf * 64, p0 = w.off + row;
+      ok = mbar_wait(&ctl.q_full[st], (t / kStages) & 1, wc, 0xa7) && mbar_wait(&ctl.s_full[hf], t & 1, wc, 0xa8);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool masked = p0 < all_first || p0 + 64 > all_last;
+      uint32_t vis[2] = {~0u, ~0u};
+      if (masked) {
+        vis[0] = bits_below(last - p0) & ~bits_below(first - p0);
+        vis[1] = bits_below(last - p0 - 32) & ~bits_below(first - p0 - 32);
+      }
+      uint64_t p[32];
+      uint32_t buf[32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(t_s + c * 32, buf);
+        tmem_ld_wait();
+        const float4* nl = reinterpret_cast<const float4*>(&stat[st][0][hf * 64 + c * 32]);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 v = nl[i];
+          const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x0, x1;
+            up2(fma2(pk2(__uint_as_float(buf[4 * i + 2 * e]), __uint_as_float(buf[4 * i + 2 * e + 1])), sl2, n2[e]), x0, x1);
+            if (masked) {
+              if (!(vis[c] & (1u << (4 * i + 2 * e)))) x0 = -INFINITY;
+              if (!(vis[c] & (1u << (4 * i + 2 * e + 1)))) x1 = -INFINITY;
+            }
+            const float e0 = ex2(x0), e1 = ex2(x1);
+            p[c * 16 + 2 * i + e] = pk2(e0, e1);
+            pk[2 * i + e] = f2_to_bf2(e0, e1);
+          }
+        }
+        // P^T of 32 queries over 16 of the columns already read
+        tmem_st16(t_s + c * 16, pk);
+      }
+      tmem_st_wait();
+      if (p0 + 64 > len && len < w.off + w.N) {
+        // padding rows of Q and dO meet P = dS = 0: zero them, whatever they hold
+        if (p0 + (r & 63) >= len) {
+          const uint32_t rr = hf * 64 + (r & 63);
+          uint8_t* base = (r < 64 ? q_s : do_s) + st * kTileB;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(base + (c >> 3) * kHalf + sw128_off(rr, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl.p_full[hf]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_ld32(t_dp + c * 32, buf);
+        tmem_ld_wait();
+        const float4* nd = reinterpret_cast<const float4*>(&stat[st][1][hf * 64 + c * 32]);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 v = nd[i];
+          const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t d = add2(pk2(__uint_as_float(buf[4 * i + 2 * e]), __uint_as_float(buf[4 * i + 2 * e + 1])), n2[e]);
+            float x0, x1;
+            up2(mul2(d, p[c * 16 + 2 * i + e]), x0, x1);
+            if (masked) {
+              if (!(vis[c] & (1u << (4 * i + 2 * e)))) x0 = 0.f;
+              if (!(vis[c] & (1u << (4 * i + 2 * e + 1)))) x1 = 0.f;
+            }
+            pk[2 * i + e] = f2_to_bf2(x0, x1);
+          }
+        }
+        tmem_st16(t_s + 32 + c * 16, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&ctl.ds_full[hf]);
+    }
+    // ---------------- epilogue: warpgroup 0 writes dV, 1 writes dK
+    if (steps > 0 && ok) {
+      ok = mbar_wait(&ctl.mm_done[0], (steps - 1) & 1, wc, 0xa9) && mbar_wait(&ctl.mm_done[1], (steps - 1) & 1, wc, 0xaa);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (ok && (parts == 1 || steps > 0)) {
+      tc_fence_after();
+      const float mul = hf ? scale : 1.f;
+      __nv_bfloat16* dst = (hf ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD;
+      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * gridDim.x + blockIdx.x) * 2 + hf) * kRows + r) * kD;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (steps > 0) {
+          tmem_ld32((hf ? t_dk : t_dv) + lane_base + c * 32, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (parts > 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(pdst + c * 32 + 4 * i) =
+                make_float4(mul * __uint_as_float(o[4 * i]), mul * __uint_as_float(o[4 * i + 1]),
+                            mul * __uint_as_float(o[4 * i + 2]), mul * __uint_as_float(o[4 * i + 3]));
+        } else if (j < w.N_keys) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = f2_to_bf2(mul * __uint_as_float(o[8 * i + 2 * e]), mul * __uint_as_float(o[8 * i + 2 * e + 1]));
+            *reinterpret_cast<uint4*>(dst + c * 32 + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    if (*wc.abort_flag && steps > 0) {  // MMAs in flight finish before TMEM is freed
+      mbar_drain(&ctl.mm_done[0], (steps - 1) & 1);
+      mbar_drain(&ctl.mm_done[1], (steps - 1) & 1);
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Sums the shares of the split key tiles in order.  One CTA per (split key tile
+// and one of dV, dK; key head; batch); thread = 4 columns of a row per pass.
+__global__ void __launch_bounds__(512)
+    window_join_kernel(const float* __restrict__ part, const WindowDev w, const DkvPlan plan,
+                       int items, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  const int hk = blockIdx.y, b = blockIdx.z, which = blockIdx.x & 1;
+  const int split_sinks = plan.sink_parts > 1 ? plan.sink_tiles : 0;
+  const int s = blockIdx.x >> 1;
+  const int kt = s < split_sinks ? s : plan.sink_tiles + (s - split_sinks);
+  const bool sink = kt < plan.sink_tiles;
+  const int item = sink ? kt * plan.sink_parts
+                        : plan.sink_tiles * plan.sink_parts + (kt - plan.sink_tiles) * plan.win_parts;
+  const QSpan qs = query_span(w, kt, window_length(w, b));
+  const int n = (w.heads / w.kv_heads * qs.count + plan.chunk - 1) / plan.chunk;  // shares written
+  const float* p = part + ((((size_t)b * w.kv_heads + hk) * items + item) * 2 + which) * kRows * kD;
+  __nv_bfloat16* dst = which ? dk : dv;
+  for (int i = threadIdx.x; i < kRows * kD / 4; i += 512) {
+    const int j = kt * kRows + i / (kD / 4);
+    if (j >= w.N_keys) break;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < n; ++k) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (size_t)k * 2 * kRows * kD) + i);
+      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(dst + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + (i % (kD / 4)) * 4) =
+        make_uint2(f2_to_bf2(a.x, a.y), f2_to_bf2(a.z, a.w));
+  }
+}
+
+// ---------------------------------------------------------------- dq
+struct DqCtl {
+  uint64_t q_full;
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], ds_full[2], mm_done[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const WindowDev w, float sl, float scale, int n_pad,
+                     const float* __restrict__ nlse, const float* __restrict__ ndelta,
+                     __nv_bfloat16* __restrict__ dq, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ DqCtl ctl;
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* q_s = smem;
+  uint8_t* do_s = q_s + kTileB;
+  uint8_t* k_s = do_s + kTileB;            // ring
+  uint8_t* v_s = k_s + kStages * kTileB;   // ring
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qt = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int hk = h / (w.heads / w.kv_heads);
+  const int row0 = qt * kRows;
+  const int len = window_length(w, b);
+  const TileSpan span = window_span(w, w.off + row0, w.off + min(row0 + kRows, w.N) - 1, len);
+  const int steps = span.count();
+  auto tile_of = [&](int t) { return t < span.ns ? t : span.w0 + t - span.ns; };
+  const WaitCtx wc{&ctl.abort_flag, status};
+
+  if (tid == 0) {
+    mbar_init(&ctl.q_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl.kv_full[i], 1);
+      mbar_init(&ctl.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.ds_full[i], 128);
+      mbar_init(&ctl.mm_done[i], 1);
+    }
+    ctl.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t t_dq = tmem + 256;  // S halves, dP halves, dQ
+
+  if (warp == kWarpProd) {
+    if (lane == 0 && steps > 0) {
+      mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
+      tma_load_3d(q_s, &tm_q, &ctl.q_full, h * kD, row0, b);
+      tma_load_3d(q_s + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0, b);
+      tma_load_3d(do_s, &tm_do, &ctl.q_full, h * kD, row0, b);
+      tma_load_3d(do_s + kHalf, &tm_do, &ctl.q_full, h * kD + 64, row0, b);
+      int n = 0;
+      for (int t = 0; t < steps; ++t) {
+        const int st = t % kStages, row = tile_of(t) * kRows;
+        if (t >= kStages && !mbar_wait(&ctl.kv_empty[st], ((t / kStages) - 1) & 1, wc, 0xb1)) break;
+        mbar_arrive_expect_tx(&ctl.kv_full[st], 2 * kTileB);
+        tma_load_3d(k_s + st * kTileB, &tm_k, &ctl.kv_full[st], hk * kD, row, b);
+        tma_load_3d(k_s + st * kTileB + kHalf, &tm_k, &ctl.kv_full[st], hk * kD + 64, row, b);
+        tma_load_3d(v_s + st * kTileB, &tm_v, &ctl.kv_full[st], hk * kD, row, b);
+        tma_load_3d(v_s + st * kTileB + kHalf, &tm_v, &ctl.kv_full[st], hk * kD + 64, row, b);
+        ++n;
+      }
+      if (*wc.abort_flag) {
+        mbar_drain(&ctl.q_full, 0);
+        for (int t = n > kStages ? n - kStages : 0; t < n; ++t) mbar_drain(&ctl.kv_full[t % kStages], (t / kStages) & 1);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    if (lane == 0 && steps > 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, 64, 0, 0);   // Q K_w^T, dO V_w^T
+      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // dS_w K_w
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t dd0 = smem_desc_sw128(smem_u32(do_s), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), 16, 1024);
+      const uint64_t mk0 = smem_desc_sw128(smem_u32(k_s), kHalf, 1024);
+      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bq, int w2) {
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_ss(d, desc_advance(a, o), desc_advance(bq, o + w2 * 8192), idesc_s, kk != 0);
+        }
+      };
+      bool ok = mbar_wait(&ctl.q_full, 0, wc, 0xb2) && mbar_wait(&ctl.kv_full[0], 0, wc, 0xb3);
+      if (ok) {
+        tc_fence_after();
+        for (int i = 0; i < 2; ++i) {
+          issue_ab(tmem + 128 + i * 64, dd0, dv0, i);
+          issue_ab(tmem + i * 64, dq0, dk0, i);
+          umma_commit(&ctl.s_full[i]);
+        }
+      }
+      for (int t = 0; ok && t < steps; ++t) {
+        const uint32_t cur = (t % kStages) * kTileB, nxt = ((t + 1) % kStages) * kTileB;
+        for (int i = 0; i < 2; ++i) {
+          ok = mbar_wait(&ctl.ds_full[i], t & 1, wc, 0xb5);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(t_dq, tmem + i * 64 + kk * 8, desc_advance(mk0, cur + i * 8192 + kk * 2048), idesc_g,
+                    (t | i | kk) != 0);
+          umma_commit(&ctl.mm_done[i]);
+          if (i == 1) umma_commit(&ctl.kv_empty[t % kStages]);
+          if (t + 1 < steps) {
+            if (i == 0) ok = mbar_wait(&ctl.kv_full[(t + 1) % kStages], ((t + 1) / kStages) & 1, wc, 0xb3);
+            if (!ok) break;
+            tc_fence_after();
+            issue_ab(tmem + 128 + i * 64, dd0, desc_advance(dv0, nxt), i);
+            ok = mbar_wait(&ctl.mm_done[i], t & 1, wc, 0xb6);  // the product that reads dS has finished
+            if (!ok) break;
+            tc_fence_after();
+            issue_ab(tmem + i * 64, dq0, desc_advance(dk0, nxt), i);
+            umma_commit(&ctl.s_full[i]);
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax warps: thread = query row
+    const int hf = warp >> 2;              // which half of the key tile
+    const int r = (warp & 3) * 32 + lane;  // query row
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + hf * 64 + lane_base, t_dp = tmem + 128 + hf * 64 + lane_base;
+    const int row = row0 + r, pos = w.off + row;
+    const int end = min(window_end(w, pos), len), low = window_low(w, window_end(w, pos));
+    const int pos1 = min(min(w.off + row0 + kRows, w.off + w.N), len) - 1;
+    const int all_end = min(window_end(w, w.off + row0), len);
+    const int all_low = window_low(w, window_end(w, max(pos1, 0)));
+    const size_t at = ((size_t)b * w.heads + h) * n_pad + row;  // row < n_pad
+    const float nl = nlse[at], nd = ndelta[at];
+    const bool live = nl != -INFINITY;
+    const uint64_t sl2 = pk2(sl, sl), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
+    bool ok = true;
+    for (int t = 0; t < steps; ++t) {
+      const int key0 = tile_of(t) * kRows + hf * 64;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[hf], t & 1, wc, 0xb8));
+      if (!ok) break;
+      tc_fence_after();
+      const bool masked = key0 + 64 > all_end || (key0 < all_low && key0 + 64 > w.sinks) || pos1 - w.off - row0 < kRows - 1;
+      uint32_t vis[2] = {~0u, ~0u};
+      if (masked) {
+        vis[0] = live ? visible_bits(key0, low, end, w.sinks) : 0u;
+        vis[1] = live ? visible_bits(key0 + 32, low, end, w.sinks) : 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t s[32], d[32], pk[16];
+        tmem_ld32(t_s + c * 32, s);
+        tmem_ld32(t_dp + c * 32, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1, g0, g1;
+          up2(fma2(pk2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl2, nl2), x0, x1);
+          const uint64_t p = pk2(ex2(x0), ex2(x1));
+          up2(mul2(add2(pk2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), nd2), p), g0, g1);
+          if (masked) {
+            if (!(vis[c] & (1u << (2 * i)))) g0 = 0.f;
+            if (!(vis[c] & (2u << (2 * i)))) g1 = 0.f;
+          }
+          pk[i] = f2_to_bf2(g0, g1);
+        }
+        tmem_st16(t_s + c * 16, pk);
+      }
+      tmem_st_wait();
+      if (key0 + 64 > len && len < w.N_keys) {
+        // padding rows of K meet dS = 0: zero them, whatever they hold
+        if (r < 64 && key0 + r >= len) {
+          uint8_t* base = k_s + (t % kStages) * kTileB;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(base + (c >> 3) * kHalf + sw128_off(hf * 64 + r, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl.ds_full[hf]);
+    }
+    // ---------------- epilogue: warpgroup 0 writes columns [0, 64), 1 the rest
+    if (steps > 0 && ok) {
+      ok = mbar_wait(&ctl.mm_done[0], (steps - 1) & 1, wc, 0xb9) && mbar_wait(&ctl.mm_done[1], (steps - 1) & 1, wc, 0xba);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (ok) {
+      tc_fence_after();
+      __nv_bfloat16* dst = dq + (((size_t)b * w.N + row) * w.heads + h) * kD + hf * 64;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t o[32];
+        if (steps > 0) {
+          tmem_ld32(t_dq + lane_base + hf * 64 + c * 32, o);
+          tmem_ld_wait();
+        }
+        if (row < w.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = live && steps > 0 ? f2_to_bf2(scale * __uint_as_float(o[8 * i + 2 * e]),
+                                                   scale * __uint_as_float(o[8 * i + 2 * e + 1]))
+                                       : 0u;
+            *reinterpret_cast<uint4*>(dst + c * 32 + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    if (*wc.abort_flag && steps > 0) {
+      mbar_drain(&ctl.mm_done[0], (steps - 1) & 1);
+      mbar_drain(&ctl.mm_done[1], (steps - 1) & 1);
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr size_t kBwdSmem = 1024 + (2 + 2 * kStages) * (size_t)kTileB;
+
+// A key tile is left whole while there are two CTAs for every SM; otherwise its
+// steps are cut so that there are, down to four steps each.  The sinks' tiles,
+// which all later queries see, are cut into shares as long as a window tile's.
+DkvPlan dkv_plan(const WindowCall& c) {
+  DkvPlan p{};
+  const int group = c.heads / c.kv_heads;
+  const long long q_tiles = (c.N + kRows - 1) / kRows;
+  p.tiles = (c.N_keys + kRows - 1) / kRows;
+  // query tiles that a key tile's window can reach
+  long long reach = q_tiles;
+  if (c.window) {
+    const long long span = ((long long)c.window + c.block + 2 * kRows - 3) / kRows + 1;
+    reach = span < q_tiles ? span : q_tiles;
+    p.sink_tiles = (c.sinks + kRows - 1) / kRows;
+    if (p.sink_tiles > p.tiles) p.sink_tiles = p.tiles;
+  }
+  const long long base = group * reach;
+  const long long ctas = (long long)p.tiles * c.kv_heads * c.B;
+  const long long parts = ctas >= 2 * kNumSMs ? 1 : (2 * kNumSMs + ctas - 1) / ctas;
+  long long chunk = (base + parts - 1) / parts;
+  if (chunk < 4) chunk = 4;
+  p.chunk = (int)chunk;
+  p.win_parts = (int)((base + chunk - 1) / chunk);
+  p.sink_parts = (int)((group * q_tiles + chunk - 1) / chunk);
+  return p;
+}
+int dkv_items(const DkvPlan& p) {
+  return p.sink_tiles * p.sink_parts + (p.tiles - p.sink_tiles) * p.win_parts;
+}
+bool dkv_split(const DkvPlan& p) {
+  return (p.sink_tiles && p.sink_parts > 1) || (p.tiles > p.sink_tiles && p.win_parts > 1);
+}
+
+struct BwdWs {
+  __nv_bfloat16* d_o;
+  float *nlse, *ndelta, *part;
+  size_t bytes;
+};
+int pad_rows(int n) { return (n + kRows - 1) / kRows * kRows; }
+BwdWs carve(const WindowCall& c, void* ws) {
+  Carver cv(ws, ~size_t(0));
+  BwdWs w{};
+  const size_t rows = (size_t)c.B * c.heads * pad_rows(c.N);
+  w.nlse = cv.take<float>(rows);
+  w.ndelta = cv.take<float>(rows);
+  if (c.gate) w.d_o = cv.take<__nv_bfloat16>((size_t)c.B * c.N * c.heads * kD);
+  const DkvPlan p = dkv_plan(c);
+  if (dkv_split(p)) w.part = cv.take<float>((size_t)c.B * c.kv_heads * dkv_items(p) * 2 * kRows * kD);
+  w.bytes = align_up(cv.used, 256);
+  return w;
+}
+
+}  // namespace
+
+size_t window_bwd_ws_bytes(const WindowCall& c) { return carve(c, nullptr).bytes; }
+
+sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse, const void* dy,
+                           void* dq, void* dk, void* dv, void* dg, void* ws, cudaStream_t st) {
+  const BwdWs m = carve(c, ws);
+  const int n_pad = pad_rows(c.N);
+  const WindowDev w{c.N, c.N_keys, c.N_keys - c.N, c.window, c.sinks, c.block, c.heads, c.kv_heads, c.lengths};
+  const uint64_t N = c.N, Nk = c.N_keys, C = (uint64_t)c.heads * kD, Ck = (uint64_t)c.kv_heads * kD;
+  const void* d_o = c.gate ? static_cast<const void*>(m.d_o) : dy;
+  CUtensorMap tq, td, tk, tv;
+  if (!make_tmap_bf16_3d(&tq, c.q, C, N, c.B, c.q_stride, N * c.q_stride, kRows) ||
+      !make_tmap_bf16_3d(&td, d_o, C, N, c.B, C, N * C, kRows) ||
+      !make_tmap_bf16_3d(&tk, c.k, Ck, Nk, c.B, c.k_stride, Nk * c.k_stride, kRows) ||
+      !make_tmap_bf16_3d(&tv, c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows))
+    return fail(SANA_ERR_CUDA, "windowed anchor backward: cuTensorMapEncodeTiled failed");
+  once_per_context(kAttrWindowBwd, [] {
+    cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
+    cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
+  });
+  using bf = __nv_bfloat16;
+  const long long rows = (long long)c.B * n_pad * c.heads;
+  const unsigned prep = (unsigned)((rows + 15) / 16);
+  if (c.gate)
+    window_prep_kernel<true><<<prep, 256, 0, st>>>((const bf*)y, (const bf*)dy, (const bf*)c.gate, c.gate_stride, lse,
+                                                   w, c.B, n_pad, m.nlse, m.ndelta, m.d_o, (bf*)dg);
+  else
+    window_prep_kernel<false><<<prep, 256, 0, st>>>((const bf*)y, (const bf*)dy, nullptr, 0, lse, w, c.B, n_pad,
+                                                    m.nlse, m.ndelta, nullptr, nullptr);
+  if (sana_status e = check_launch("window_prep_kernel")) return e;
+  const float sl = c.scale * kLog2e;
+  int* sw = status_word();
+  const DkvPlan p = dkv_plan(c);
+  const int items = dkv_items(p);
+  window_dkv_kernel<<<dim3(items, c.kv_heads, c.B), kThreads, kBwdSmem, st>>>(
+      tq, td, tk, tv, w, p, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dk, (bf*)dv, sw);
+  if (sana_status e = check_launch("window_dkv_kernel")) return e;
+  const int split = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.win_parts > 1 ? p.tiles - p.sink_tiles : 0);
+  if (split) {
+    window_join_kernel<<<dim3(2 * split, c.kv_heads, c.B), 512, 0, st>>>(m.part, w, p, items, (bf*)dk, (bf*)dv);
+    if (sana_status e = check_launch("window_join_kernel")) return e;
+  }
+  window_dq_kernel<<<dim3((c.N + kRows - 1) / kRows, c.heads, c.B), kThreads, kBwdSmem, st>>>(
+      tq, td, tk, tv, w, sl, c.scale, n_pad, m.nlse, m.ndelta, (bf*)dq, sw);
+  return check_launch("window_dq_kernel");
+}
+
+}  // namespace sana

@@ -1,0 +1,520 @@
+// Windowed softmax anchor, forward, bf16 on tcgen05 (the mask: window.cuh).
+//
+//   Y_i = sigmoid(G_i) * sum_j p_ij V_j,  p_ij = exp(s_ij - lse_i) over the
+//   visible j,  s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij).
+//
+// One pass over the visible key tiles with a running maximum and sum in fp32
+// (base 2; the sum is taken over the fp32 exponentials, which are then rounded
+// to bf16 as the A operand of P V: each rounding is 2^-9 of its term and they
+// average out).
+//
+// One CTA per (batch, query head, pair of 128-query tiles); the two tiles share
+// the K and V tiles in shared memory, and their softmax warpgroups alternate
+// with the tensor core:
+//   producer warp : TMA Q_0, Q_1 once; K_u, V_u in two-stage rings over the key
+//                   tiles that either query tile sees (sinks, then the window);
+//                   the gate at the end, into the K ring
+//   MMA warp      : for each of them, where query tile i sees it: O_i += P_i V,
+//                   and S_i = Q_i K^T of the next one
+//   2 x 4 softmax warps (thread = query row): mask (only tiles that some row of
+//                   the query tile sees in part), row max, exponentials, P over
+//                   its S columns, lazy rescaling of O in TMEM (when a row's max
+//                   grows by more than 2^8), 1/l, gate, lse and the TMA store.
+// TMEM (512 columns): S_0 S_1 O_0 O_1, 128 each; P_i over the first half of S_i.
+//
+// Bound by the tensor core (4 * 128 flops per pair and head) with the MUFU unit
+// close behind: a quarter of the exponentials run as a cubic on the FMA pipe.
+#include <cuda.h>
+
+#include "f32x2.cuh"
+#include "sana_internal.h"
+#include "window.cuh"
+
+namespace sana {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kRows = kWinTile;
+constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
+constexpr int kTileB = 2 * kHalf;      // 32 KB
+constexpr int kKS = 2, kVS = 2;        // K and V stages
+constexpr int kThreads = 320;          // 8 softmax warps + producer + MMA
+constexpr int kWarpProd = 8, kWarpMma = 9;
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kEmuPairs = 2;           // of every 8 pairs of exponentials, on the FMA pipe
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^(sl * s - m) for two scores on the FMA pipe, m an integer below 2^22 in
+// magnitude.  c = 1.5 * 2^23 - m: t = sl s + c holds n = round(sl s - m) in its
+// low mantissa bits, f = sl s - (t - c) lies in [-1/2, 1/2], 2^f is a cubic
+// fitted for it (7.5e-5 relative, far below the bf16 step of P), and n is added
+// to the exponent field.  Scores below s_lo = (m - 126) / sl count as s_lo:
+// 2^-126 instead of less, nothing beside the row's largest term.
+__device__ __forceinline__ void exp2_scaled2(float s0, float s1, float s_lo, uint64_t sl, uint64_t c,
+                                             float& y0, float& y1) {
+  const uint64_t s = pk2(fmaxf(s0, s_lo), fmaxf(s1, s_lo));
+  const uint64_t t = fma2(s, sl, c);
+  const uint64_t d = sub2(c, t);  // -(n + m)
+  const uint64_t f = fma2(s, sl, d);
+  uint64_t p = fma2(pk2(0.055170517f, 0.055170517f), f, pk2(0.24260856f, 0.24260856f));
+  p = fma2(p, f, pk2(0.69326097f, 0.69326097f));
+  p = fma2(p, f, pk2(0.99992824f, 0.99992824f));
+  float t0, t1, p0, p1;
+  up2(t, t0, t1);
+  up2(p, p0, p1);
+  uint32_t r0, r1;
+  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r0) : "r"(__float_as_uint(t0)), "r"(__float_as_uint(p0)));
+  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r1) : "r"(__float_as_uint(t1)), "r"(__float_as_uint(p1)));
+  y0 = __uint_as_float(r0);
+  y1 = __uint_as_float(r1);
+}
+
+struct WinCtl {
+  uint64_t q_full, g_full;
+  uint64_t k_full[kKS], k_empty[kKS];
+  uint64_t v_full[kVS], v_empty[kVS];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t ysync[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+// The key tiles of a CTA: those that either query tile sees, sinks first.
+struct PairSpan {
+  TileSpan s[2];
+  int ns, w0, n;
+  __device__ __forceinline__ int tile(int u) const { return u < ns ? u : w0 + (u - ns); }
+  __device__ __forceinline__ bool active(int i, int u) const { return u < n && s[i].has(tile(u)); }
+};
+__device__ __forceinline__ PairSpan pair_span(const WindowDev& w, int row0, int len) {
+  PairSpan p;
+  int last = -1;
+  p.w0 = 0x7fffffff;
+  p.ns = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int a = row0 + i * kRows, b = min(a + kRows, w.N) - 1;
+    p.s[i] = window_span(w, w.off + a, w.off + b, len);
+    if (p.s[i].w1 >= p.s[i].w0) {
+      p.w0 = min(p.w0, p.s[i].w0);
+      last = max(last, p.s[i].w1);
+      p.ns = max(p.ns, p.s[i].ns);
+    }
+  }
+  p.ns = min(p.ns, p.w0);
+  p.n = last < 0 ? 0 : p.ns + last - p.w0 + 1;
+  return p;
+}
+
+template <bool kGate>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
+                      const __grid_constant__ CUtensorMap tm_y, const WindowDev w, float sl,
+                      float* __restrict__ lse, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WinCtl ctl;
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* q_s = smem;                // Q_0, Q_1 (later: Y staging)
+  uint8_t* k_s = q_s + 2 * kTileB;    // K ring (later: gate tiles)
+  uint8_t* v_s = k_s + kKS * kTileB;  // V ring
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the last query tiles see the most keys where the window is open: they start first
+  const int qp = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int hk = h / (w.heads / w.kv_heads);
+  const int row0 = qp * 2 * kRows;
+  const int len = window_length(w, b);
+  const PairSpan span = pair_span(w, row0, len);
+  const WaitCtx wc{&ctl.abort_flag, status};
+
+  if (tid == 0) {
+    mbar_init(&ctl.q_full, 1);
+    mbar_init(&ctl.g_full, 1);
+    for (int i = 0; i < kKS; ++i) {
+      mbar_init(&ctl.k_full[i], 1);
+      mbar_init(&ctl.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVS; ++i) {
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 128);
+      mbar_init(&ctl.pv_done[i], 1);
+      mbar_init(&ctl.ysync[i], 128);
+    }
+    ctl.abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+
+  if (warp == kWarpProd) {
+    // ------------------------------------------------ TMA producer
+    if (lane == 0 && span.n > 0) {
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+      mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
+      for (int i = 0; i < 2; ++i) {  // a tile past N reads as zeros
+        tma_load_3d(q_s + i * kTileB, &tm_q, &ctl.q_full, h * kD, row0 + i * kRows, b);
+        tma_load_3d(q_s + i * kTileB + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0 + i * kRows, b);
+      }
+      int nk = 0, nv = 0;
+      bool ok = true;
+      for (int u = 0; u < span.n; ++u) {
+        const int sk = u % kKS, sv = u % kVS;
+        const int row = span.tile(u) * kRows;
+        if (u >= kKS && !mbar_wait(&ctl.k_empty[sk], ((u / kKS) - 1) & 1, wc, 0x91)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
+        tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
+        tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
+        ++nk;
+        if (u >= kVS && !mbar_wait(&ctl.v_empty[sv], ((u / kVS) - 1) & 1, wc, 0x92)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
+        tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
+        tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
+        ++nv;
+      }
+      // the gate goes into the K ring once the last S products have read it
+      if (ok && kGate) {
+        for (int u = (span.n > kKS ? span.n - kKS : 0); u < span.n && ok; ++u)
+          ok = mbar_wait(&ctl.k_empty[u % kKS], (u / kKS) & 1, wc, 0x9c);
+        if (ok) {
+          mbar_arrive_expect_tx(&ctl.g_full, 2 * kTileB);
+          for (int i = 0; i < 2; ++i) {
+            tma_load_3d(k_s + i * kTileB, &tm_g, &ctl.g_full, h * kD, row0 + i * kRows, b);
+            tma_load_3d(k_s + i * kTileB + kHalf, &tm_g, &ctl.g_full, h * kD + 64, row0 + i * kRows, b);
+          }
+        }
+      }
+      if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
+        mbar_drain(&ctl.q_full, 0);
+        for (int u = nk > kKS ? nk - kKS : 0; u < nk; ++u) mbar_drain(&ctl.k_full[u % kKS], (u / kKS) & 1);
+        for (int u = nv > kVS ? nv - kVS : 0; u < nv; ++u) mbar_drain(&ctl.v_full[u % kVS], (u / kVS) & 1);
+        if (ok && kGate) mbar_drain(&ctl.g_full, 0);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0 && span.n > 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, both K-major
+      const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
+      int done[2] = {0, 0};  // P V products issued for each query tile
+      auto issue_s = [&](int i, int u) {
+        const uint64_t a = desc_advance(dq0, i * kTileB);
+        const uint64_t bk = desc_advance(dk0, (u % kKS) * kTileB);
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_ss(tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc_s, kk != 0);
+        }
+        umma_commit(&ctl.s_full[i]);
+      };
+      auto issue_pv = [&](int i, int u) {
+        const uint64_t bv = desc_advance(dv0, (u % kVS) * kTileB);
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+                  (done[i] | kk) != 0);
+        umma_commit(&ctl.pv_done[i]);
+      };
+      bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
+      if (ok) {
+        tc_fence_after();
+        for (int i = 0; i < 2; ++i)
+          if (span.active(i, 0)) issue_s(i, 0);
+        umma_commit(&ctl.k_empty[0]);
+      }
+      for (int u = 0; ok && u < span.n; ++u) {
+        const bool more = u + 1 < span.n;
+        if (!mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x95)) break;
+        if (more && !mbar_wait(&ctl.k_full[(u + 1) % kKS], ((u + 1) / kKS) & 1, wc, 0x96)) break;
+        for (int i = 0; i < 2; ++i) {
+          if (span.active(i, u)) {
+            // P_i is in TMEM and O_i has been rescaled if needed
+            if (!mbar_wait(&ctl.p_full[i], done[i] & 1, wc, 0x94)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_pv(i, u);
+            ++done[i];
+          }
+          if (span.active(i, u + 1)) {
+            // S_i is overwritten once the product that reads P_i from it has finished
+            if (done[i] && !mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_s(i, u + 1);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&ctl.v_empty[u % kVS]);
+        if (more) umma_commit(&ctl.k_empty[(u + 1) % kKS]);
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax warps: thread = query row
+    const int qi = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tmem_s = tmem + qi * 128, tmem_o = tmem + 256 + qi * 128;
+    const int row = row0 + qi * kRows + r;
+    const int pos = w.off + row;
+    const bool row_live = row < w.N && pos < len;
+    // this row's limits, and those of the tile's first and last live rows
+    const int end = min(window_end(w, pos), len), low = window_low(w, window_end(w, pos));
+    const int pos0 = w.off + row0 + qi * kRows;
+    const int pos1 = min(min(pos0 + kRows, w.off + w.N), len) - 1;
+    const int all_end = min(window_end(w, pos0), len);       // every live row sees below it
+    const int all_low = window_low(w, window_end(w, max(pos1, 0)));  // every live row sees from it on
+    const uint64_t sl2 = pk2(sl, sl);
+    const float inv_sl = 1.f / sl;
+    float m = -INFINITY, l = 0.f;  // row max reference and sum, base 2
+    bool ok = true;
+    int done = 0;
+    for (int u = 0; ok && u < span.n; ++u) {
+      if (!span.active(qi, u)) continue;
+      const int key0 = span.tile(u) * kRows;
+      if (!__all_sync(0xffffffffu, mbar_wait(&ctl.s_full[qi], done & 1, wc, 0x98))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool masked = key0 + kRows > all_end || (key0 < all_low && key0 + kRows > w.sinks);
+      uint32_t vis[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) vis[c] = masked ? visible_bits(key0 + 32 * c, low, end, w.sinks) : ~0u;
+      // pass 1: row max of the raw scores
+      float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t sa[32], sb[32];
+        tmem_ld32(tmem_s + lane_base + hh * 64, sa);
+        tmem_ld32(tmem_s + lane_base + hh * 64 + 32, sb);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (!(vis[2 * hh] & (1u << i))) sa[i] = __float_as_uint(-INFINITY);
+            if (!(vis[2 * hh + 1] & (1u << i))) sb[i] = __float_as_uint(-INFINITY);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            mq[a] = max3(mq[a], __uint_as_float(sa[i + 2 * a]), __uint_as_float(sb[i + 2 * a + 1]));
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+            mq[a] = max3(mq[a], __uint_as_float(sa[i + 2 * a + 1]), __uint_as_float(sb[i + 2 * a]));
+      }
+      const float m_new = fmaxf(m, sl * max3(mq[0], mq[1], fmaxf(mq[2], mq[3])));
+      // lazy rescaling: the reference moves only when the max grew by more than
+      // 2^8 (the decision to touch O is warp-uniform: TMEM access is
+      // warp-collective).  It is rounded up to an integer for the folded
+      // constants of exp2_scaled2.  A row that has seen no key yet keeps -inf
+      // and works against 0: its terms are all 2^-inf (or 2^-126, dropped by
+      // the factor 0 when its first key comes).
+      const bool grow = m_new > m + kRescaleLog2;
+      const bool any_grow = __any_sync(0xffffffffu, grow);
+      const float m_next = grow ? ceilf(m_new) : m;
+      const float corr = grow ? ex2(m - m_next) : 1.f;
+      const float m_use = m_next == -INFINITY ? 0.f : m_next;
+      const uint64_t neg_m = pk2(-m_use, -m_use);
+      const uint64_t cfold = pk2(12582912.f - m_use, 12582912.f - m_use);
+      const float s_lo = (m_use - 126.f) * inv_sl;
+      // pass 2: P over 32-column chunks, the next chunk's load in flight
+      uint64_t rs2 = pk2(0.f, 0.f);
+      uint32_t sc[2][32];
+      uint32_t pk[32];
+      tmem_ld32(tmem_s + lane_base, sc[0]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c < 3) tmem_ld32(tmem_s + lane_base + (c + 1) * 32, sc[(c + 1) & 1]);
+        uint32_t* cur = sc[c & 1];
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(vis[c] & (1u << i))) cur[i] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float s0 = __uint_as_float(cur[i]), s1 = __uint_as_float(cur[i + 1]);
+          float p0, p1;
+          if (((i >> 1) & 7) >= 8 - kEmuPairs) {
+            exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
+          } else {
+            float x0, x1;
+            up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
+            p0 = ex2(x0);
+            p1 = ex2(x1);
+          }
+          rs2 = add2(rs2, pk2(p0, p1));
+          pk[(c & 1) * 16 + i / 2] = f2_to_bf2(p0, p1);
+        }
+        if (c & 1) tmem_st32(tmem_s + lane_base + (c >> 1) * 32, pk);
+        if (c < 3) tmem_ld_wait();
+      }
+      float rs0, rs1;
+      up2(rs2, rs0, rs1);
+      l = l * corr + (rs0 + rs1);
+      m = m_next;
+      if (any_grow && done >= 1) {
+        // O_i holds the sum over the tiles before this one
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x99))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem_o + lane_base + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+          tmem_st32(tmem_o + lane_base + c * 32, o);
+        }
+      }
+      tmem_st_wait();
+      if (key0 + kRows > len && len < w.N_keys) {
+        // padding rows of V meet P = 0: zero them, whatever they hold (both
+        // warpgroups write the same zeros before their own product reads V)
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x9d))) {
+          ok = false;
+          break;
+        }
+        uint8_t* vt = v_s + (u % kVS) * kTileB;
+        if (key0 + r >= len) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl.p_full[qi]);
+      ++done;
+    }
+    // ---------------- epilogue
+    const bool any = span.s[qi].count() > 0;
+    ok = __all_sync(0xffffffffu, ok && (!any || (done > 0 && mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x9a))));
+    if (kGate && span.n > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl.g_full, 0, wc, 0x9d));
+    uint8_t* ybuf = q_s + qi * kTileB;  // Q_i is no longer read
+    const uint8_t* gbuf = k_s + qi * kTileB;
+    if (ok) {
+      tc_fence_after();
+      const bool some = row_live && l > 0.f;
+      const float inv = some ? 1.f / l : 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (any) {  // else nothing was accumulated for this tile
+          tmem_ld32(tmem_o + lane_base + c * 32, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int ch = (c & 1) * 4 + q;
+          const uint32_t off = (c >> 1) * kHalf + sw128_off(r, ch);
+          uint32_t gw[4] = {0, 0, 0, 0};
+          if (kGate && some) {
+            const uint4 gr = *reinterpret_cast<const uint4*>(gbuf + off);
+            gw[0] = gr.x; gw[1] = gr.y; gw[2] = gr.z; gw[3] = gr.w;
+          }
+          uint32_t out[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y0 = __uint_as_float(o[q * 8 + 2 * i]) * inv;
+            float y1 = __uint_as_float(o[q * 8 + 2 * i + 1]) * inv;
+            if (kGate) {
+              const float2 gg = bf2_to_f2(gw[i]);
+              y0 *= sigmoid_fast(gg.x);
+              y1 *= sigmoid_fast(gg.y);
+            }
+            out[i] = some ? f2_to_bf2(y0, y1) : 0u;
+          }
+          *reinterpret_cast<uint4*>(ybuf + off) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+      }
+      if (lse && row < w.N)
+        lse[((size_t)b * w.heads + h) * w.N + row] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+      fence_proxy_async_smem();
+    }
+    mbar_arrive(&ctl.ysync[qi]);
+    ok = mbar_wait(&ctl.ysync[qi], 0, wc, 0x9b) && ok;
+    if (ok && r == 0 && row0 + qi * kRows < w.N) {  // a tile past N has nothing to store
+      tma_store_3d(&tm_y, ybuf, h * kD, row0 + qi * kRows, b);
+      tma_store_3d(&tm_y, ybuf + kHalf, h * kD + 64, row0 + qi * kRows, b);
+      bulk_commit();
+      bulk_wait0();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    if (*wc.abort_flag) {  // MMAs in flight finish before TMEM is freed
+      for (int i = 0; i < 2; ++i) {
+        const int n = span.s[i].count();
+        if (n) mbar_drain(&ctl.pv_done[i], (n - 1) & 1);
+      }
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr size_t kWinSmem = 1024 + 2 * kTileB + kKS * kTileB + kVS * kTileB;
+
+}  // namespace
+
+sana_status window_fwd_run(const WindowCall& c, float* lse, void* out, cudaStream_t st) {
+  const uint64_t N = c.N, Nk = c.N_keys, C = (uint64_t)c.heads * kD, Ck = (uint64_t)c.kv_heads * kD;
+  CUtensorMap tq, tk, tv, tg, ty;
+  bool okm = make_tmap_bf16_3d(&tq, c.q, C, N, c.B, c.q_stride, N * c.q_stride, kRows) &&
+             make_tmap_bf16_3d(&tk, c.k, Ck, Nk, c.B, c.k_stride, Nk * c.k_stride, kRows) &&
+             make_tmap_bf16_3d(&tv, c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows) &&
+             make_tmap_bf16_3d(&ty, out, C, N, c.B, C, N * C, kRows);
+  if (c.gate) okm = okm && make_tmap_bf16_3d(&tg, c.gate, C, N, c.B, c.gate_stride, N * c.gate_stride, kRows);
+  else tg = tq;
+  if (!okm) return fail(SANA_ERR_CUDA, "windowed anchor: cuTensorMapEncodeTiled failed");
+  once_per_context(kAttrWindowFwd, [] {
+    cudaFuncSetAttribute(window_fwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWinSmem);
+    cudaFuncSetAttribute(window_fwd_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWinSmem);
+  });
+  const WindowDev w{c.N, c.N_keys, c.N_keys - c.N, c.window, c.sinks, c.block, c.heads, c.kv_heads, c.lengths};
+  const dim3 grid((c.N + 2 * kRows - 1) / (2 * kRows), c.heads, c.B);
+  const float sl = c.scale * 1.4426950408889634f;
+  int* sw = status_word();
+  if (c.gate)
+    window_fwd_kernel<true><<<grid, kThreads, kWinSmem, st>>>(tq, tk, tv, tg, ty, w, sl, lse, sw);
+  else
+    window_fwd_kernel<false><<<grid, kThreads, kWinSmem, st>>>(tq, tk, tv, tg, ty, w, sl, lse, sw);
+  return check_launch("window_fwd_kernel");
+}
+
+}  // namespace sana
