@@ -16,10 +16,14 @@
 //                   the gate at the end, into the K ring
 //   MMA warp      : for each of them, where query tile i sees it: O_i += P_i V,
 //                   and S_i = Q_i K^T of the next one
-//   2 x 4 softmax warps (thread = query row): mask (only tiles that some row of
-//                   the query tile sees in part), row max, exponentials, P over
-//                   its S columns, lazy rescaling of O in TMEM (when a row's max
-//                   grows by more than 2^8), 1/l, gate, lse and the TMA store.
+//   2 x 4 softmax warps (thread = query row): the score row in registers, masked
+//                   where some row of the query tile sees the key tile in part;
+//                   row max, lazy rescaling of O in TMEM (where a max passes the
+//                   reference by more than 2^16), exponentials, P over its S
+//                   columns in two halves, each handed on at once; at the end
+//                   1/l, gate, lse and the TMA store.
+// Registers: a softmax thread holds 128 scores, more than the 168 registers of
+// an even share, so the other warps give some of theirs up.
 // TMEM (512 columns): S_0 S_1 O_0 O_1, 128 each; P_i over the first half of S_i.
 //
 // Bound by the tensor core (4 * 128 flops per pair and head) with the MUFU unit
@@ -38,9 +42,12 @@ constexpr int kRows = kWinTile;
 constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
 constexpr int kTileB = 2 * kHalf;      // 32 KB
 constexpr int kKS = 2, kVS = 2;        // K and V stages
-constexpr int kThreads = 320;          // 8 softmax warps + producer + MMA
+constexpr int kThreads = 384;          // 8 softmax warps, producer, MMA, two idle warps
 constexpr int kWarpProd = 8, kWarpMma = 9;
-constexpr float kRescaleLog2 = 8.f;
+// Registers a thread: 168 at launch; the softmax warps take more from the others.
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "more registers than at launch");
+constexpr float kRescaleLog2 = 16.f;
 constexpr int kEmuPairs = 2;           // of every 8 pairs of exponentials, on the FMA pipe
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -73,7 +80,7 @@ struct WinCtl {
   uint64_t q_full, g_full;
   uint64_t k_full[kKS], k_empty[kKS];
   uint64_t v_full[kVS], v_empty[kVS];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2];  // p_full[tile][half of the keys]
   uint64_t ysync[2];
   uint32_t tmem;
   int abort_flag;
@@ -141,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], 128);
+      mbar_init(&ctl.p_full[i][0], 128);
+      mbar_init(&ctl.p_full[i][1], 128);
       mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.ysync[i], 128);
     }
@@ -157,124 +165,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
 
-  if (warp == kWarpProd) {
-    // ------------------------------------------------ TMA producer
-    if (lane == 0 && span.n > 0) {
-      prefetch_tmap(&tm_q);
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-      mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
-      for (int i = 0; i < 2; ++i) {  // a tile past N reads as zeros
-        tma_load_3d(q_s + i * kTileB, &tm_q, &ctl.q_full, h * kD, row0 + i * kRows, b);
-        tma_load_3d(q_s + i * kTileB + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0 + i * kRows, b);
-      }
-      int nk = 0, nv = 0;
-      bool ok = true;
-      for (int u = 0; u < span.n; ++u) {
-        const int sk = u % kKS, sv = u % kVS;
-        const int row = span.tile(u) * kRows;
-        if (u >= kKS && !mbar_wait(&ctl.k_empty[sk], ((u / kKS) - 1) & 1, wc, 0x91)) {
-          ok = false;
-          break;
+  if (warp >= kWarpProd) {
+    warpgroup_regs_dec<kRegsOther>();
+    if (warp == kWarpProd) {
+      // ------------------------------------------------ TMA producer
+      if (lane == 0 && span.n > 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
+        for (int i = 0; i < 2; ++i) {  // a tile past N reads as zeros
+          tma_load_3d(q_s + i * kTileB, &tm_q, &ctl.q_full, h * kD, row0 + i * kRows, b);
+          tma_load_3d(q_s + i * kTileB + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0 + i * kRows, b);
         }
-        mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
-        tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
-        tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
-        ++nk;
-        if (u >= kVS && !mbar_wait(&ctl.v_empty[sv], ((u / kVS) - 1) & 1, wc, 0x92)) {
-          ok = false;
-          break;
+        int nk = 0, nv = 0;
+        bool ok = true;
+        for (int u = 0; u < span.n; ++u) {
+          const int sk = u % kKS, sv = u % kVS;
+          const int row = span.tile(u) * kRows;
+          if (u >= kKS && !mbar_wait(&ctl.k_empty[sk], ((u / kKS) - 1) & 1, wc, 0x91)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
+          tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
+          tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
+          ++nk;
+          if (u >= kVS && !mbar_wait(&ctl.v_empty[sv], ((u / kVS) - 1) & 1, wc, 0x92)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
+          tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
+          tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
+          ++nv;
         }
-        mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
-        tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
-        tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
-        ++nv;
+        // the gate goes into the K ring once the last S products have read it
+        if (ok && kGate) {
+          for (int u = (span.n > kKS ? span.n - kKS : 0); u < span.n && ok; ++u)
+            ok = mbar_wait(&ctl.k_empty[u % kKS], (u / kKS) & 1, wc, 0x9c);
+          if (ok) {
+            mbar_arrive_expect_tx(&ctl.g_full, 2 * kTileB);
+            for (int i = 0; i < 2; ++i) {
+              tma_load_3d(k_s + i * kTileB, &tm_g, &ctl.g_full, h * kD, row0 + i * kRows, b);
+              tma_load_3d(k_s + i * kTileB + kHalf, &tm_g, &ctl.g_full, h * kD + 64, row0 + i * kRows, b);
+            }
+          }
+        }
+        if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
+          mbar_drain(&ctl.q_full, 0);
+          for (int u = nk > kKS ? nk - kKS : 0; u < nk; ++u) mbar_drain(&ctl.k_full[u % kKS], (u / kKS) & 1);
+          for (int u = nv > kVS ? nv - kVS : 0; u < nv; ++u) mbar_drain(&ctl.v_full[u % kVS], (u / kVS) & 1);
+          if (ok && kGate) mbar_drain(&ctl.g_full, 0);
+        }
       }
-      // the gate goes into the K ring once the last S products have read it
-      if (ok && kGate) {
-        for (int u = (span.n > kKS ? span.n - kKS : 0); u < span.n && ok; ++u)
-          ok = mbar_wait(&ctl.k_empty[u % kKS], (u / kKS) & 1, wc, 0x9c);
+    } else if (warp == kWarpMma) {
+      // ------------------------------------------------ MMA issuer
+      if (span.n > 0) {  // the whole warp, its elected lane issues
+        const uint32_t lead = elect_lead();
+        const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, both K-major
+        const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
+        const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
+        int done[2] = {0, 0};  // P V products issued for each query tile
+        auto issue_s = [&](int i, int u) {
+          const uint64_t a = desc_local(desc_advance(dq0, i * kTileB));
+          const uint64_t bk = desc_local(desc_advance(dk0, (u % kKS) * kTileB));
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+            umma_ss_lead(lead, tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc_s, kk != 0);
+          }
+          umma_commit_lead(lead, &ctl.s_full[i]);
+        };
+        auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys
+          const uint64_t bv = desc_local(desc_advance(dv0, (u % kVS) * kTileB + half * 8192));
+          const uint32_t ap = tmem + i * 128 + half * 32;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts_lead(lead, tmem + 256 + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+                         (done[i] | half | kk) != 0);
+        };
+        bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
         if (ok) {
-          mbar_arrive_expect_tx(&ctl.g_full, 2 * kTileB);
+          tc_fence_after();
+          for (int i = 0; i < 2; ++i)
+            if (span.active(i, 0)) issue_s(i, 0);
+          umma_commit_lead(lead, &ctl.k_empty[0]);
+        }
+        for (int u = 0; ok && u < span.n; ++u) {
+          const bool more = u + 1 < span.n;
+          if (!mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x95)) break;
+          if (more && !mbar_wait(&ctl.k_full[(u + 1) % kKS], ((u + 1) / kKS) & 1, wc, 0x96)) break;
           for (int i = 0; i < 2; ++i) {
-            tma_load_3d(k_s + i * kTileB, &tm_g, &ctl.g_full, h * kD, row0 + i * kRows, b);
-            tma_load_3d(k_s + i * kTileB + kHalf, &tm_g, &ctl.g_full, h * kD + 64, row0 + i * kRows, b);
-          }
-        }
-      }
-      if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
-        mbar_drain(&ctl.q_full, 0);
-        for (int u = nk > kKS ? nk - kKS : 0; u < nk; ++u) mbar_drain(&ctl.k_full[u % kKS], (u / kKS) & 1);
-        for (int u = nv > kVS ? nv - kVS : 0; u < nv; ++u) mbar_drain(&ctl.v_full[u % kVS], (u / kVS) & 1);
-        if (ok && kGate) mbar_drain(&ctl.g_full, 0);
-      }
-    }
-  } else if (warp == kWarpMma) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0 && span.n > 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, both K-major
-      const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
-      const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
-      int done[2] = {0, 0};  // P V products issued for each query tile
-      auto issue_s = [&](int i, int u) {
-        const uint64_t a = desc_advance(dq0, i * kTileB);
-        const uint64_t bk = desc_advance(dk0, (u % kKS) * kTileB);
-#pragma unroll
-        for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_ss(tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc_s, kk != 0);
-        }
-        umma_commit(&ctl.s_full[i]);
-      };
-      auto issue_pv = [&](int i, int u) {
-        const uint64_t bv = desc_advance(dv0, (u % kVS) * kTileB);
-#pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
-          umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
-                  (done[i] | kk) != 0);
-        umma_commit(&ctl.pv_done[i]);
-      };
-      bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
-      if (ok) {
-        tc_fence_after();
-        for (int i = 0; i < 2; ++i)
-          if (span.active(i, 0)) issue_s(i, 0);
-        umma_commit(&ctl.k_empty[0]);
-      }
-      for (int u = 0; ok && u < span.n; ++u) {
-        const bool more = u + 1 < span.n;
-        if (!mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x95)) break;
-        if (more && !mbar_wait(&ctl.k_full[(u + 1) % kKS], ((u + 1) / kKS) & 1, wc, 0x96)) break;
-        for (int i = 0; i < 2; ++i) {
-          if (span.active(i, u)) {
-            // P_i is in TMEM and O_i has been rescaled if needed
-            if (!mbar_wait(&ctl.p_full[i], done[i] & 1, wc, 0x94)) {
-              ok = false;
-              break;
+            if (span.active(i, u)) {
+              // P_i is in TMEM, half by half, and O_i has been rescaled if needed
+              for (int half = 0; half < 2; ++half) {
+                if (!mbar_wait(&ctl.p_full[i][half], done[i] & 1, wc, 0x94)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                issue_pv(i, u, half);
+              }
+              if (!ok) break;
+              umma_commit_lead(lead, &ctl.pv_done[i]);
+              ++done[i];
             }
-            tc_fence_after();
-            issue_pv(i, u);
-            ++done[i];
-          }
-          if (span.active(i, u + 1)) {
-            // S_i is overwritten once the product that reads P_i from it has finished
-            if (done[i] && !mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97)) {
-              ok = false;
-              break;
+            if (span.active(i, u + 1)) {
+              // S_i is overwritten once the product that reads P_i from it has finished
+              if (done[i] && !mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              issue_s(i, u + 1);
             }
-            tc_fence_after();
-            issue_s(i, u + 1);
           }
+          if (!ok) break;
+          umma_commit_lead(lead, &ctl.v_empty[u % kVS]);
+          if (more) umma_commit_lead(lead, &ctl.k_empty[(u + 1) % kKS]);
         }
-        if (!ok) break;
-        umma_commit(&ctl.v_empty[u % kVS]);
-        if (more) umma_commit(&ctl.k_empty[(u + 1) % kKS]);
       }
     }
   } else {
     // ------------------------------------------------ softmax warps: thread = query row
+    warpgroup_regs_inc<kRegsSoftmax>();
     const int qi = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -302,106 +319,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       const bool masked = key0 + kRows > all_end || (key0 < all_low && key0 + kRows > w.sinks);
-      uint32_t vis[4];
+      uint32_t sc[4][32];  // the whole row
 #pragma unroll
-      for (int c = 0; c < 4; ++c) vis[c] = masked ? visible_bits(key0 + 32 * c, low, end, w.sinks) : ~0u;
-      // pass 1: row max of the raw scores
-      float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      for (int c = 0; c < 4; ++c) tmem_ld32(tmem_s + lane_base + c * 32, sc[c]);
+      tmem_ld_wait();
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t sa[32], sb[32];
-        tmem_ld32(tmem_s + lane_base + hh * 64, sa);
-        tmem_ld32(tmem_s + lane_base + hh * 64 + 32, sb);
-        tmem_ld_wait();
-        if (masked) {
+      for (int c = 0; c < 4; ++c) tmem_tie(sc[c]);
+      auto chunk_max = [&](const uint32_t (&x)[32], float t) {  // two chains of 3-input max
+        float t2 = __uint_as_float(x[0]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (!(vis[2 * hh] & (1u << i))) sa[i] = __float_as_uint(-INFINITY);
-            if (!(vis[2 * hh + 1] & (1u << i))) sb[i] = __float_as_uint(-INFINITY);
+        for (int i = 1; i < 31; i += 4) {
+          t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          if (i + 3 < 32) t2 = max3(t2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+        }
+        return max3(t, t2, __uint_as_float(x[31]));
+      };
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t vis = visible_bits(key0 + 32 * c, low, end, w.sinks);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(vis & (1u << i))) sc[c][i] = __float_as_uint(-INFINITY);
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) top = chunk_max(sc[c], top);
+      top *= sl;
+      // The reference moves where the row's max passes it, on its first key or
+      // by more than 2^16.  It is rounded up to an integer for the folded
+      // constants of exp2_scaled2.  A row that has seen no key yet keeps -inf
+      // and works against 0: its terms are 2^-inf (or 2^-126, dropped by the
+      // factor 0 when its first key comes).
+      const bool grow = top > m + kRescaleLog2;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float m_next = grow ? ceilf(top) : m;
+        const float corr = grow ? ex2(m - m_next) : 1.f;
+        m = m_next;
+        l *= corr;
+        if (done >= 1) {
+          // O_i holds the sum over the tiles before this one (warp-uniform:
+          // TMEM access is warp-collective)
+          if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x99))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tmem_o + lane_base + c * 16, o);
+            tmem_ld_wait();
+            tmem_tie(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+            tmem_st16(tmem_o + lane_base + c * 16, o);
           }
         }
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-            mq[a] = max3(mq[a], __uint_as_float(sa[i + 2 * a]), __uint_as_float(sb[i + 2 * a + 1]));
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-            mq[a] = max3(mq[a], __uint_as_float(sa[i + 2 * a + 1]), __uint_as_float(sb[i + 2 * a]));
       }
-      const float m_new = fmaxf(m, sl * max3(mq[0], mq[1], fmaxf(mq[2], mq[3])));
-      // lazy rescaling: the reference moves only when the max grew by more than
-      // 2^8 (the decision to touch O is warp-uniform: TMEM access is
-      // warp-collective).  It is rounded up to an integer for the folded
-      // constants of exp2_scaled2.  A row that has seen no key yet keeps -inf
-      // and works against 0: its terms are all 2^-inf (or 2^-126, dropped by
-      // the factor 0 when its first key comes).
-      const bool grow = m_new > m + kRescaleLog2;
-      const bool any_grow = __any_sync(0xffffffffu, grow);
-      const float m_next = grow ? ceilf(m_new) : m;
-      const float corr = grow ? ex2(m - m_next) : 1.f;
-      const float m_use = m_next == -INFINITY ? 0.f : m_next;
+      const float m_use = m == -INFINITY ? 0.f : m;
       const uint64_t neg_m = pk2(-m_use, -m_use);
       const uint64_t cfold = pk2(12582912.f - m_use, 12582912.f - m_use);
       const float s_lo = (m_use - 126.f) * inv_sl;
-      // pass 2: P over 32-column chunks, the next chunk's load in flight
       uint64_t rs2 = pk2(0.f, 0.f);
-      uint32_t sc[2][32];
-      uint32_t pk[32];
-      tmem_ld32(tmem_s + lane_base, sc[0]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c < 3) tmem_ld32(tmem_s + lane_base + (c + 1) * 32, sc[(c + 1) & 1]);
-        uint32_t* cur = sc[c & 1];
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(vis[c] & (1u << i))) cur[i] = __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float s0 = __uint_as_float(cur[i]), s1 = __uint_as_float(cur[i + 1]);
-          float p0, p1;
-          if (((i >> 1) & 7) >= 8 - kEmuPairs) {
-            exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
-          } else {
-            float x0, x1;
-            up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
-            p0 = ex2(x0);
-            p1 = ex2(x1);
-          }
-          rs2 = add2(rs2, pk2(p0, p1));
-          pk[(c & 1) * 16 + i / 2] = f2_to_bf2(p0, p1);
-        }
-        if (c & 1) tmem_st32(tmem_s + lane_base + (c >> 1) * 32, pk);
-        if (c < 3) tmem_ld_wait();
-      }
-      float rs0, rs1;
-      up2(rs2, rs0, rs1);
-      l = l * corr + (rs0 + rs1);
-      m = m_next;
-      if (any_grow && done >= 1) {
-        // O_i holds the sum over the tiles before this one
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x99))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem_o + lane_base + c * 32, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-          tmem_st32(tmem_o + lane_base + c * 32, o);
-        }
-      }
-      tmem_st_wait();
-      if (key0 + kRows > len && len < w.N_keys) {
+      const bool tail = key0 + kRows > len && len < w.N_keys;
+      if (tail) {
         // padding rows of V meet P = 0: zero them, whatever they hold (both
         // warpgroups write the same zeros before their own product reads V)
         if (!__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x9d))) {
@@ -416,14 +399,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
       }
-      tc_fence_before();
-      mbar_arrive(&ctl.p_full[qi]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float s0 = __uint_as_float(sc[c][i]), s1 = __uint_as_float(sc[c][i + 1]);
+          float p0, p1;
+          if (((i >> 1) & 7) >= 8 - kEmuPairs) {
+            exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
+          } else {
+            float x0, x1;
+            up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
+            p0 = ex2(x0);
+            p1 = ex2(x1);
+          }
+          rs2 = add2(rs2, pk2(p0, p1));
+          pk[i / 2] = f2_to_bf2(p0, p1);
+        }
+        // over S columns that are in registers; after each half of the keys the
+        // product with V may start on it
+        tmem_st16(tmem_s + lane_base + c * 16, pk);
+        if (c & 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&ctl.p_full[qi][c >> 1]);
+        }
+      }
+      float rs0, rs1;
+      up2(rs2, rs0, rs1);
+      l += rs0 + rs1;
       ++done;
     }
     // ---------------- epilogue
     const bool any = span.s[qi].count() > 0;
     ok = __all_sync(0xffffffffu, ok && (!any || (done > 0 && mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x9a))));
-    if (kGate && span.n > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl.g_full, 0, wc, 0x9d));
+    // Q_i becomes the output's staging: its load has landed before the first S,
+    // and where this tile had none, it is waited for here
+    if (!any && span.n > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl.q_full, 0, wc, 0x9f));
+    if (kGate && span.n > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl.g_full, 0, wc, 0x9e));
     uint8_t* ybuf = q_s + qi * kTileB;  // Q_i is no longer read
     const uint8_t* gbuf = k_s + qi * kTileB;
     if (ok) {
