@@ -21,12 +21,16 @@
 // over the key tiles, 64 KB through L2 for every tile pair, in an order to be
 // enforced.
 //
-// dkv and dq share one plan: a 128 x 128 tile pair is done in two halves of 64
-// columns, each with its own softmax warpgroup and its own S and dP columns in
-// TMEM, so the tensor core works for one half while the other's exponentials
-// run.  P and dS go over the S columns, so a half's dP columns are free as soon
-// as dS is written: the next dP product is issued there at once and covers the
-// wait for the products that still read P and dS.
+// dkv and dq share one plan: whole 128 x 128 products (a product of 64 columns
+// reads its 128-row A operand from shared memory for half the work, and took
+// three times as long), one tile pair at a time, and 16 softmax warps (thread =
+// row and 32 columns) whose two phases -- exponentials, then dS -- run while the
+// tensor core does the products that do not need their result:
+//   dkv    tensor: dV(t) | S(t+1) | dK(t) | dP(t+1)     warps: dS(t) | P(t+1)
+//          (P over the S columns, dS over the dP columns)
+//   dq     tensor: dP(t+1) | dQ(t) | S(t+2)             warps: dS(t) | P(t+1)
+//          (two S buffers; dS over the S columns of its tile)
+// A product that overwrites what another reads waits for it by its barrier.
 #include <cuda.h>
 
 #include "f32x2.cuh"
@@ -40,15 +44,41 @@ constexpr int kD = 128;
 constexpr int kRows = kWinTile;
 constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
 constexpr int kTileB = 2 * kHalf;      // 32 KB
-constexpr int kStages = 2;
-constexpr int kThreads = 320;          // 8 softmax warps + producer + MMA
-constexpr int kWarpProd = 8, kWarpMma = 9;
+constexpr int kDeep = 3, kShort = 2;    // stages of the ring whose tiles live long / short
+constexpr int kThreads = 576;          // 16 softmax warps + producer + MMA
+constexpr int kSoft = 512;             // softmax threads
+constexpr int kWarpProd = 16, kWarpMma = 17;
+// of every 8 pairs of exponentials, on the FMA pipe (the MUFU unit alone would
+// take as long as two of the four products that hide it)
+constexpr int kEmuPairs = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 2^x for two x <= 0 (or a little above) on the FMA pipe: n = round(x) in the low
+// mantissa bits of x + 1.5 * 2^23, a cubic on [-1/2, 1/2] (7.5e-5 relative), n
+// added to the exponent.  Below -126 counts as -126: nothing in bf16 or beside 1.
+__device__ __forceinline__ void exp2_pair(uint64_t x, float& y0, float& y1) {
+  float a, b;
+  up2(x, a, b);
+  const uint64_t v = pk2(fmaxf(a, -126.f), fmaxf(b, -126.f)), c = pk2(12582912.f, 12582912.f);
+  const uint64_t t = add2(v, c);
+  const uint64_t f = sub2(v, sub2(t, c));
+  uint64_t p = fma2(pk2(0.055170517f, 0.055170517f), f, pk2(0.24260856f, 0.24260856f));
+  p = fma2(p, f, pk2(0.69326097f, 0.69326097f));
+  p = fma2(p, f, pk2(0.99992824f, 0.99992824f));
+  float t0, t1, p0, p1;
+  up2(t, t0, t1);
+  up2(p, p0, p1);
+  uint32_t r0, r1;
+  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r0) : "r"(__float_as_uint(t0)), "r"(__float_as_uint(p0)));
+  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r1) : "r"(__float_as_uint(t1)), "r"(__float_as_uint(p1)));
+  y0 = __uint_as_float(r0);
+  y1 = __uint_as_float(r1);
 }
 
 // Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16 bytes).
@@ -154,11 +184,15 @@ struct DkvPlan {
 
 struct DkvCtl {
   uint64_t kv_full;
-  uint64_t q_full[kStages], q_empty[kStages];
-  uint64_t s_full[2], p_full[2], ds_full[2], mm_done[2];
+  uint64_t q_full[kDeep], q_empty[kDeep];      // Q tiles
+  uint64_t do_full[kShort], do_empty[kShort];  // do tiles and row statistics
+  uint64_t s_full, dp_full, p_full, ds_full, dv_done, dk_done;
   uint32_t tmem;
   int abort_flag;
 };
+// Dynamic shared memory: K, V, Q ring, do ring (each tile a multiple of 1024
+// bytes from the 1024-aligned start), row statistics of each do stage.
+constexpr size_t kDkvSmem = (2 + kDeep + kShort) * (size_t)kTileB + kShort * 2 * kRows * sizeof(float);
 
 __global__ void __launch_bounds__(kThreads, 1)
     window_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -167,14 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const float* __restrict__ nlse, const float* __restrict__ ndelta,
                       float* __restrict__ part, __nv_bfloat16* __restrict__ dk,
                       __nv_bfloat16* __restrict__ dv, int* status) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ DkvCtl ctl;
-  __shared__ __align__(16) float stat[kStages][2][kRows];
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* k_s = smem;
   uint8_t* v_s = k_s + kTileB;
-  uint8_t* q_s = v_s + kTileB;              // ring of query tiles
-  uint8_t* do_s = q_s + kStages * kTileB;   // ring of their do tiles
+  uint8_t* q_s = v_s + kTileB;
+  uint8_t* do_s = q_s + kDeep * kTileB;
+  float* stat = reinterpret_cast<float*>(do_s + kShort * kTileB);  // [stage][-lse, -delta][row]
+  DkvCtl& ctl = *reinterpret_cast<DkvCtl*>(stat + kShort * 2 * kRows);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y, b = blockIdx.z, group = w.heads / w.kv_heads;
@@ -202,16 +235,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&ctl.kv_full, 1);
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kDeep; ++i) {
       mbar_init(&ctl.q_full[i], 1);
       mbar_init(&ctl.q_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], 128);
-      mbar_init(&ctl.ds_full[i], 128);
-      mbar_init(&ctl.mm_done[i], 1);
+    for (int i = 0; i < kShort; ++i) {
+      mbar_init(&ctl.do_full[i], 1);
+      mbar_init(&ctl.do_empty[i], 1);
     }
+    mbar_init(&ctl.s_full, 1);
+    mbar_init(&ctl.dp_full, 1);
+    mbar_init(&ctl.p_full, kSoft);
+    mbar_init(&ctl.ds_full, kSoft);
+    mbar_init(&ctl.dv_done, 1);
+    mbar_init(&ctl.dk_done, 1);
     ctl.abort_flag = 0;
     mbar_fence_init();
   }
@@ -223,8 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  // columns: S^T halves [0,64) [64,128), dP^T halves [128,192) [192,256), dV, dK
-  const uint32_t t_dv = tmem + 256, t_dk = tmem + 384;
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 384;
 
   if (warp == kWarpProd) {
     if (lane == 0 && steps > 0) {
@@ -233,200 +269,232 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_3d(k_s + kHalf, &tm_k, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
       tma_load_3d(v_s, &tm_v, &ctl.kv_full, hk * kD, kt * kRows, b);
       tma_load_3d(v_s + kHalf, &tm_v, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
-      int n = 0;
+      int nq = 0, nd = 0;
       for (int t = 0; t < steps; ++t) {
-        const int st = t % kStages, h = head_of(t), row = qrow_of(t);
-        if (t >= kStages && !mbar_wait(&ctl.q_empty[st], ((t / kStages) - 1) & 1, wc, 0xa1)) break;
-        mbar_arrive_expect_tx(&ctl.q_full[st], 2 * kTileB + 2 * kRows * 4);
-        tma_load_3d(q_s + st * kTileB, &tm_q, &ctl.q_full[st], h * kD, row, b);
-        tma_load_3d(q_s + st * kTileB + kHalf, &tm_q, &ctl.q_full[st], h * kD + 64, row, b);
-        tma_load_3d(do_s + st * kTileB, &tm_do, &ctl.q_full[st], h * kD, row, b);
-        tma_load_3d(do_s + st * kTileB + kHalf, &tm_do, &ctl.q_full[st], h * kD + 64, row, b);
+        const int sq = t % kDeep, sd = t % kShort, h = head_of(t), row = qrow_of(t);
+        if (t >= kDeep && !mbar_wait(&ctl.q_empty[sq], ((t / kDeep) - 1) & 1, wc, 0xa1)) break;
+        mbar_arrive_expect_tx(&ctl.q_full[sq], kTileB);
+        tma_load_3d(q_s + sq * kTileB, &tm_q, &ctl.q_full[sq], h * kD, row, b);
+        tma_load_3d(q_s + sq * kTileB + kHalf, &tm_q, &ctl.q_full[sq], h * kD + 64, row, b);
+        ++nq;
+        // a do slot is free once dV has read it, its statistics' slot once dS is
+        // made, which dK's end (q_empty) implies
+        if (t >= kShort && (!mbar_wait(&ctl.do_empty[sd], ((t / kShort) - 1) & 1, wc, 0xab) ||
+                            !mbar_wait(&ctl.q_empty[(t - kShort) % kDeep], ((t - kShort) / kDeep) & 1, wc, 0xb0)))
+          break;
         const size_t at = ((size_t)b * w.heads + h) * n_pad + row;
-        bulk_load(stat[st][0], nlse + at, kRows * 4, &ctl.q_full[st]);
-        bulk_load(stat[st][1], ndelta + at, kRows * 4, &ctl.q_full[st]);
-        ++n;
+        mbar_arrive_expect_tx(&ctl.do_full[sd], kTileB + 2 * kRows * 4);
+        tma_load_3d(do_s + sd * kTileB, &tm_do, &ctl.do_full[sd], h * kD, row, b);
+        tma_load_3d(do_s + sd * kTileB + kHalf, &tm_do, &ctl.do_full[sd], h * kD + 64, row, b);
+        bulk_load(stat + sd * 2 * kRows, nlse + at, kRows * 4, &ctl.do_full[sd]);
+        bulk_load(stat + sd * 2 * kRows + kRows, ndelta + at, kRows * 4, &ctl.do_full[sd]);
+        ++nd;
       }
       if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
         mbar_drain(&ctl.kv_full, 0);
-        for (int t = n > kStages ? n - kStages : 0; t < n; ++t) mbar_drain(&ctl.q_full[t % kStages], (t / kStages) & 1);
+        for (int t = nq > kDeep ? nq - kDeep : 0; t < nq; ++t) mbar_drain(&ctl.q_full[t % kDeep], (t / kDeep) & 1);
+        for (int t = nd > kShort ? nd - kShort : 0; t < nd; ++t) mbar_drain(&ctl.do_full[t % kShort], (t / kShort) & 1);
       }
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0 && steps > 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(128, 64, 0, 0);   // K Q_w^T, V dO_w^T
-      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // P^T dO_w, dS^T Q_w (rows of B along K)
+    if (steps > 0) {  // the whole warp, its elected lane issues
+      const uint32_t lead = elect_lead();
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // K Q^T, V do^T
+      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // P^T do, dS^T Q (rows of B along K)
       const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), 16, 1024);
       const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
       const uint64_t dd0 = smem_desc_sw128(smem_u32(do_s), 16, 1024);
       const uint64_t mq0 = smem_desc_sw128(smem_u32(q_s), kHalf, 1024);
       const uint64_t md0 = smem_desc_sw128(smem_u32(do_s), kHalf, 1024);
-      // D (128 x 64) = A B_w^T over the 64 rows of half w
-      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bq, int w2) {
+      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bt) {  // D = A B^T
+        a = desc_local(a);
+        bt = desc_local(bt);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_ss(d, desc_advance(a, o), desc_advance(bq, o + w2 * 8192), idesc_s, kk != 0);
+          umma_ss_lead(lead, d, desc_advance(a, o), desc_advance(bt, o), idesc_s, kk != 0);
         }
       };
-      // D (128 x 128) += A_w (TMEM) B over the 64 rows of half w
-      auto issue_acc = [&](uint32_t d, uint32_t a, uint64_t bm, int w2, bool acc) {
+      // D += A B, A in TMEM: the 32 columns of each warp quarter over the first
+      // half of its 32 score columns
+      auto issue_acc = [&](uint32_t d, uint32_t a, uint64_t bm, bool acc) {
+        bm = desc_local(bm);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ts(d, a + kk * 8, desc_advance(bm, w2 * 8192 + kk * 2048), idesc_g, acc || kk != 0);
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          umma_ts_lead(lead, d, a + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bm, kk * 2048), idesc_g, acc || kk != 0);
       };
       bool ok = mbar_wait(&ctl.kv_full, 0, wc, 0xa2) && mbar_wait(&ctl.q_full[0], 0, wc, 0xa3);
       if (ok) {
         tc_fence_after();
-        for (int i = 0; i < 2; ++i) {
-          issue_ab(tmem + 128 + i * 64, dv0, dd0, i);
-          issue_ab(tmem + i * 64, dk0, dq0, i);
-          umma_commit(&ctl.s_full[i]);
-        }
+        issue_ab(t_s, dk0, dq0);
+        umma_commit_lead(lead, &ctl.s_full);
+        ok = mbar_wait(&ctl.do_full[0], 0, wc, 0xac);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_ab(t_dp, dv0, dd0);
+        umma_commit_lead(lead, &ctl.dp_full);
       }
       for (int t = 0; ok && t < steps; ++t) {
-        const uint32_t cur = (t % kStages) * kTileB, nxt = ((t + 1) % kStages) * kTileB;
-        for (int i = 0; i < 2; ++i) {
-          ok = mbar_wait(&ctl.p_full[i], t & 1, wc, 0xa4);
-          if (!ok) break;
+        const bool more = t + 1 < steps;
+        const uint32_t qc = (t % kDeep) * kTileB, qn = ((t + 1) % kDeep) * kTileB;
+        const uint32_t dc = (t % kShort) * kTileB, dn = ((t + 1) % kShort) * kTileB;
+        if (!mbar_wait(&ctl.p_full, t & 1, wc, 0xa4)) break;
+        tc_fence_after();
+        issue_acc(t_dv, t_s, desc_advance(md0, dc), t > 0);
+        umma_commit_lead(lead, &ctl.dv_done);
+        umma_commit_lead(lead, &ctl.do_empty[t % kShort]);
+        if (more) {
+          if (!mbar_wait(&ctl.q_full[(t + 1) % kDeep], ((t + 1) / kDeep) & 1, wc, 0xa3) ||
+              !mbar_wait(&ctl.dv_done, t & 1, wc, 0xa6))
+            break;
           tc_fence_after();
-          issue_acc(t_dv, tmem + i * 64, desc_advance(md0, cur), i, t > 0 || i > 0);
-          ok = mbar_wait(&ctl.ds_full[i], t & 1, wc, 0xa5);
-          if (!ok) break;
+          issue_ab(t_s, dk0, desc_advance(dq0, qn));
+          umma_commit_lead(lead, &ctl.s_full);
+        }
+        if (!mbar_wait(&ctl.ds_full, t & 1, wc, 0xa5)) break;
+        tc_fence_after();
+        issue_acc(t_dk, t_dp, desc_advance(mq0, qc), t > 0);
+        umma_commit_lead(lead, &ctl.dk_done);
+        umma_commit_lead(lead, &ctl.q_empty[t % kDeep]);
+        if (more) {
+          if (!mbar_wait(&ctl.do_full[(t + 1) % kShort], ((t + 1) / kShort) & 1, wc, 0xac) ||
+              !mbar_wait(&ctl.dk_done, t & 1, wc, 0xad))
+            break;
           tc_fence_after();
-          issue_acc(t_dk, tmem + i * 64 + 32, desc_advance(mq0, cur), i, t > 0 || i > 0);
-          umma_commit(&ctl.mm_done[i]);
-          if (i == 1) umma_commit(&ctl.q_empty[t % kStages]);
-          if (t + 1 < steps) {
-            if (i == 0) ok = mbar_wait(&ctl.q_full[(t + 1) % kStages], ((t + 1) / kStages) & 1, wc, 0xa3);
-            if (!ok) break;
-            tc_fence_after();
-            issue_ab(tmem + 128 + i * 64, dv0, desc_advance(dd0, nxt), i);
-            // the products that read P and dS of this half have finished
-            ok = mbar_wait(&ctl.mm_done[i], t & 1, wc, 0xa6);
-            if (!ok) break;
-            tc_fence_after();
-            issue_ab(tmem + i * 64, dk0, desc_advance(dq0, nxt), i);
-            umma_commit(&ctl.s_full[i]);
-          }
+          issue_ab(t_dp, dv0, desc_advance(dd0, dn));
+          umma_commit_lead(lead, &ctl.dp_full);
         }
       }
     }
   } else {
-    // ------------------------------------------------ softmax warps: thread = key row
-    const int hf = warp >> 2;              // which half of the query tile
+    // ------------------------------------------------ softmax warps: thread = key row, 32 queries
+    const int cg = warp >> 2;              // which quarter of the query tile
     const int r = (warp & 3) * 32 + lane;  // key row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + hf * 64 + lane_base, t_dp = tmem + 128 + hf * 64 + lane_base;
+    const uint32_t my_s = t_s + cg * 32 + lane_base, my_dp = t_dp + cg * 32 + lane_base;
     const int j0 = kt * kRows, j = j0 + r;
     const int q_end = min(w.off + w.N, len);
     const int first = key_first(w, j), last = j < len ? min(key_last(w, j), q_end) : 0;
+    // every key of the tile is seen from all_first on, up to all_last
     const int all_first = key_first(w, j0 + kRows - 1);
     const int all_last = j0 + kRows <= len ? min(j0 + kRows <= w.sinks ? 0x7fffffff : key_last(w, max(j0, w.sinks)), q_end) : 0;
     const uint64_t sl2 = pk2(sl, sl);
     bool ok = true;
     for (int t = 0; t < steps; ++t) {
-      const int st = t % kStages;
-      const int row = qrow_of(t) + hf * 64, p0 = w.off + row;
-      ok = mbar_wait(&ctl.q_full[st], (t / kStages) & 1, wc, 0xa7) && mbar_wait(&ctl.s_full[hf], t & 1, wc, 0xa8);
+      const int sq = t % kDeep, sd = t % kShort;
+      const int p0 = w.off + qrow_of(t) + cg * 32;
+      const float* st = stat + sd * 2 * kRows + cg * 32;
+      ok = mbar_wait(&ctl.do_full[sd], (t / kShort) & 1, wc, 0xa7) && mbar_wait(&ctl.s_full, t & 1, wc, 0xa8);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const bool masked = p0 < all_first || p0 + 64 > all_last;
-      uint32_t vis[2] = {~0u, ~0u};
-      if (masked) {
-        vis[0] = bits_below(last - p0) & ~bits_below(first - p0);
-        vis[1] = bits_below(last - p0 - 32) & ~bits_below(first - p0 - 32);
-      }
-      uint64_t p[32];
-      uint32_t buf[32];
+      const bool masked = p0 < all_first || p0 + 32 > all_last;
+      const uint32_t vis = masked ? bits_below(last - p0) & ~bits_below(first - p0) : ~0u;
+      uint32_t buf[32], pk[16];
+      tmem_ld32(my_s, buf);
+      tmem_ld_wait();
+      tmem_tie(buf);
+      float p[32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld32(t_s + c * 32, buf);
-        tmem_ld_wait();
-        const float4* nl = reinterpret_cast<const float4*>(&stat[st][0][hf * 64 + c * 32]);
-        uint32_t pk[16];
+      for (int i = 0; i < 32; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(st + i);
+        const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 v = nl[i];
-          const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x0, x1;
-            up2(fma2(pk2(__uint_as_float(buf[4 * i + 2 * e]), __uint_as_float(buf[4 * i + 2 * e + 1])), sl2, n2[e]), x0, x1);
-            if (masked) {
-              if (!(vis[c] & (1u << (4 * i + 2 * e)))) x0 = -INFINITY;
-              if (!(vis[c] & (1u << (4 * i + 2 * e + 1)))) x1 = -INFINITY;
-            }
-            const float e0 = ex2(x0), e1 = ex2(x1);
-            p[c * 16 + 2 * i + e] = pk2(e0, e1);
-            pk[2 * i + e] = f2_to_bf2(e0, e1);
+        for (int e = 0; e < 2; ++e) {
+          const int k = i + 2 * e;
+          const uint64_t x = fma2(pk2(__uint_as_float(buf[k]), __uint_as_float(buf[k + 1])), sl2, n2[e]);
+          if (((k >> 1) & 7) >= 8 - kEmuPairs) {
+            exp2_pair(x, p[k], p[k + 1]);
+          } else {
+            up2(x, p[k], p[k + 1]);
+            p[k] = ex2(p[k]);
+            p[k + 1] = ex2(p[k + 1]);
           }
         }
-        // P^T of 32 queries over 16 of the columns already read
-        tmem_st16(t_s + c * 16, pk);
       }
-      tmem_st_wait();
-      if (p0 + 64 > len && len < w.off + w.N) {
-        // padding rows of Q and dO meet P = dS = 0: zero them, whatever they hold
-        if (p0 + (r & 63) >= len) {
-          const uint32_t rr = hf * 64 + (r & 63);
-          uint8_t* base = (r < 64 ? q_s : do_s) + st * kTileB;
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(vis & (1u << i))) p[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = f2_to_bf2(p[2 * i], p[2 * i + 1]);
+      tmem_st16(my_s, pk);  // over columns already read
+      const bool pad = p0 + 32 > len && len < w.off + w.N;
+      if (pad) {
+        // padding rows of do meet P = 0: zero them, whatever they hold (do is
+        // read only by the products that wait for p_full from here on)
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dp_full, t & 1, wc, 0xae));
+        if (!ok) break;
+        if (r < 32 && p0 + r >= len) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(base + (c >> 3) * kHalf + sw128_off(rr, c & 7)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(do_s + sd * kTileB + (c >> 3) * kHalf + sw128_off(cg * 32 + r, c & 7)) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&ctl.p_full[hf]);
+      mbar_arrive(&ctl.p_full);
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dp_full, t & 1, wc, 0xaf));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(my_dp, buf);
+      tmem_ld_wait();
+      tmem_tie(buf);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_ld32(t_dp + c * 32, buf);
-        tmem_ld_wait();
-        const float4* nd = reinterpret_cast<const float4*>(&stat[st][1][hf * 64 + c * 32]);
-        uint32_t pk[16];
+      for (int i = 0; i < 32; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(st + kRows + i);
+        const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 v = nd[i];
-          const uint64_t n2[2] = {pk2(v.x, v.y), pk2(v.z, v.w)};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t d = add2(pk2(__uint_as_float(buf[4 * i + 2 * e]), __uint_as_float(buf[4 * i + 2 * e + 1])), n2[e]);
-            float x0, x1;
-            up2(mul2(d, p[c * 16 + 2 * i + e]), x0, x1);
-            if (masked) {
-              if (!(vis[c] & (1u << (4 * i + 2 * e)))) x0 = 0.f;
-              if (!(vis[c] & (1u << (4 * i + 2 * e + 1)))) x1 = 0.f;
-            }
-            pk[2 * i + e] = f2_to_bf2(x0, x1);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const int k = i + 2 * e;
+          const uint64_t d = add2(pk2(__uint_as_float(buf[k]), __uint_as_float(buf[k + 1])), n2[e]);
+          up2(mul2(d, pk2(p[k], p[k + 1])), p[k], p[k + 1]);
         }
-        tmem_st16(t_s + 32 + c * 16, pk);
+      }
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(vis & (1u << i))) p[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = f2_to_bf2(p[2 * i], p[2 * i + 1]);
+      tmem_st16(my_dp, pk);
+      if (pad) {  // and padding rows of Q meet dS = 0 (S of this tile is done)
+        if (r < 32 && p0 + r >= len) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(q_s + sq * kTileB + (c >> 3) * kHalf + sw128_off(cg * 32 + r, c & 7)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&ctl.ds_full[hf]);
+      mbar_arrive(&ctl.ds_full);
     }
-    // ---------------- epilogue: warpgroup 0 writes dV, 1 writes dK
+    // ---------------- epilogue: quarters 0, 1 write dV, 2, 3 dK, 64 columns each
     if (steps > 0 && ok) {
-      ok = mbar_wait(&ctl.mm_done[0], (steps - 1) & 1, wc, 0xa9) && mbar_wait(&ctl.mm_done[1], (steps - 1) & 1, wc, 0xaa);
+      ok = mbar_wait(&ctl.dk_done, (steps - 1) & 1, wc, 0xa9) && mbar_wait(&ctl.dv_done, (steps - 1) & 1, wc, 0xaa);
       ok = __all_sync(0xffffffffu, ok);
     }
     if (ok && (parts == 1 || steps > 0)) {
       tc_fence_after();
-      const float mul = hf ? scale : 1.f;
-      __nv_bfloat16* dst = (hf ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD;
-      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * gridDim.x + blockIdx.x) * 2 + hf) * kRows + r) * kD;
+      const int which = cg >> 1, col = (cg & 1) * 64;
+      const float mul = which ? scale : 1.f;
+      __nv_bfloat16* dst = (which ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + col;
+      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * gridDim.x + blockIdx.x) * 2 + which) * kRows + r) * kD + col;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t o[32];
         if (steps > 0) {
-          tmem_ld32((hf ? t_dk : t_dv) + lane_base + c * 32, o);
+          tmem_ld32((which ? t_dk : t_dv) + lane_base + col + c * 32, o);
           tmem_ld_wait();
+          tmem_tie(o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0;
@@ -454,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == kWarpMma) {
     if (*wc.abort_flag && steps > 0) {  // MMAs in flight finish before TMEM is freed
-      mbar_drain(&ctl.mm_done[0], (steps - 1) & 1);
-      mbar_drain(&ctl.mm_done[1], (steps - 1) & 1);
+      mbar_drain(&ctl.dv_done, (steps - 1) & 1);
+      mbar_drain(&ctl.dk_done, (steps - 1) & 1);
     }
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -494,11 +562,14 @@ __global__ void __launch_bounds__(512)
 // ---------------------------------------------------------------- dq
 struct DqCtl {
   uint64_t q_full;
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], ds_full[2], mm_done[2];
+  uint64_t k_full[kDeep], k_empty[kDeep];
+  uint64_t v_full[kShort], v_empty[kShort];
+  uint64_t s_full[2], dp_full, ds_full, dq_done;
   uint32_t tmem;
   int abort_flag;
 };
+// Dynamic shared memory: Q, do, K ring, V ring.
+constexpr size_t kDqSmem = (2 + kDeep + kShort) * (size_t)kTileB;
 
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -506,13 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const WindowDev w, float sl, float scale, int n_pad,
                      const float* __restrict__ nlse, const float* __restrict__ ndelta,
                      __nv_bfloat16* __restrict__ dq, int* status) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ DqCtl ctl;
-  uint8_t* smem = align1024(smem_raw);
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_s = smem;
   uint8_t* do_s = q_s + kTileB;
-  uint8_t* k_s = do_s + kTileB;            // ring
-  uint8_t* v_s = k_s + kStages * kTileB;   // ring
+  uint8_t* k_s = do_s + kTileB;
+  uint8_t* v_s = k_s + kDeep * kTileB;
+  DqCtl& ctl = *reinterpret_cast<DqCtl*>(v_s + kShort * kTileB);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qt = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
@@ -526,15 +596,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&ctl.q_full, 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&ctl.kv_full[i], 1);
-      mbar_init(&ctl.kv_empty[i], 1);
+    for (int i = 0; i < kDeep; ++i) {
+      mbar_init(&ctl.k_full[i], 1);
+      mbar_init(&ctl.k_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.ds_full[i], 128);
-      mbar_init(&ctl.mm_done[i], 1);
+    for (int i = 0; i < kShort; ++i) {
+      mbar_init(&ctl.v_full[i], 1);
+      mbar_init(&ctl.v_empty[i], 1);
     }
+    mbar_init(&ctl.s_full[0], 1);
+    mbar_init(&ctl.s_full[1], 1);
+    mbar_init(&ctl.dp_full, 1);
+    mbar_init(&ctl.ds_full, kSoft);
+    mbar_init(&ctl.dq_done, 1);
     ctl.abort_flag = 0;
     mbar_fence_init();
   }
@@ -546,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  const uint32_t t_dq = tmem + 256;  // S halves, dP halves, dQ
+  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;  // S buffers at 0 and 128
 
   if (warp == kWarpProd) {
     if (lane == 0 && steps > 0) {
@@ -555,83 +629,104 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_3d(q_s + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0, b);
       tma_load_3d(do_s, &tm_do, &ctl.q_full, h * kD, row0, b);
       tma_load_3d(do_s + kHalf, &tm_do, &ctl.q_full, h * kD + 64, row0, b);
-      int n = 0;
+      int nk = 0, nv = 0;
       for (int t = 0; t < steps; ++t) {
-        const int st = t % kStages, row = tile_of(t) * kRows;
-        if (t >= kStages && !mbar_wait(&ctl.kv_empty[st], ((t / kStages) - 1) & 1, wc, 0xb1)) break;
-        mbar_arrive_expect_tx(&ctl.kv_full[st], 2 * kTileB);
-        tma_load_3d(k_s + st * kTileB, &tm_k, &ctl.kv_full[st], hk * kD, row, b);
-        tma_load_3d(k_s + st * kTileB + kHalf, &tm_k, &ctl.kv_full[st], hk * kD + 64, row, b);
-        tma_load_3d(v_s + st * kTileB, &tm_v, &ctl.kv_full[st], hk * kD, row, b);
-        tma_load_3d(v_s + st * kTileB + kHalf, &tm_v, &ctl.kv_full[st], hk * kD + 64, row, b);
-        ++n;
+        const int sk = t % kDeep, sv = t % kShort, row = tile_of(t) * kRows;
+        if (t >= kDeep && !mbar_wait(&ctl.k_empty[sk], ((t / kDeep) - 1) & 1, wc, 0xb1)) break;
+        mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
+        tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
+        tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
+        ++nk;
+        if (t >= kShort && !mbar_wait(&ctl.v_empty[sv], ((t / kShort) - 1) & 1, wc, 0xbb)) break;
+        mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
+        tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
+        tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
+        ++nv;
       }
       if (*wc.abort_flag) {
         mbar_drain(&ctl.q_full, 0);
-        for (int t = n > kStages ? n - kStages : 0; t < n; ++t) mbar_drain(&ctl.kv_full[t % kStages], (t / kStages) & 1);
+        for (int t = nk > kDeep ? nk - kDeep : 0; t < nk; ++t) mbar_drain(&ctl.k_full[t % kDeep], (t / kDeep) & 1);
+        for (int t = nv > kShort ? nv - kShort : 0; t < nv; ++t) mbar_drain(&ctl.v_full[t % kShort], (t / kShort) & 1);
       }
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0 && steps > 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(128, 64, 0, 0);   // Q K_w^T, dO V_w^T
-      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // dS_w K_w
+    if (steps > 0) {  // the whole warp, its elected lane issues
+      const uint32_t lead = elect_lead();
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, do V^T
+      const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // dS K
       const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
       const uint64_t dd0 = smem_desc_sw128(smem_u32(do_s), 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), 16, 1024);
       const uint64_t mk0 = smem_desc_sw128(smem_u32(k_s), kHalf, 1024);
-      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bq, int w2) {
+      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bt) {  // D = A B^T
+        a = desc_local(a);
+        bt = desc_local(bt);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_ss(d, desc_advance(a, o), desc_advance(bq, o + w2 * 8192), idesc_s, kk != 0);
+          umma_ss_lead(lead, d, desc_advance(a, o), desc_advance(bt, o), idesc_s, kk != 0);
         }
       };
-      bool ok = mbar_wait(&ctl.q_full, 0, wc, 0xb2) && mbar_wait(&ctl.kv_full[0], 0, wc, 0xb3);
+      auto issue_s = [&](int t) {
+        issue_ab(tmem + (t & 1) * 128, dq0, desc_advance(dk0, (t % kDeep) * kTileB));
+        umma_commit_lead(lead, &ctl.s_full[t & 1]);
+      };
+      auto issue_dp = [&](int t) {
+        issue_ab(t_dp, dd0, desc_advance(dv0, (t % kShort) * kTileB));
+        umma_commit_lead(lead, &ctl.dp_full);
+        umma_commit_lead(lead, &ctl.v_empty[t % kShort]);
+      };
+      bool ok = mbar_wait(&ctl.q_full, 0, wc, 0xb2) && mbar_wait(&ctl.k_full[0], 0, wc, 0xb3);
       if (ok) {
         tc_fence_after();
-        for (int i = 0; i < 2; ++i) {
-          issue_ab(tmem + 128 + i * 64, dd0, dv0, i);
-          issue_ab(tmem + i * 64, dq0, dk0, i);
-          umma_commit(&ctl.s_full[i]);
+        issue_s(0);
+        ok = mbar_wait(&ctl.v_full[0], 0, wc, 0xbc);
+      }
+      if (ok) {
+        tc_fence_after();
+        issue_dp(0);
+      }
+      if (ok && steps > 1) {
+        ok = mbar_wait(&ctl.k_full[1], 0, wc, 0xb3);
+        if (ok) {
+          tc_fence_after();
+          issue_s(1);
         }
       }
       for (int t = 0; ok && t < steps; ++t) {
-        const uint32_t cur = (t % kStages) * kTileB, nxt = ((t + 1) % kStages) * kTileB;
-        for (int i = 0; i < 2; ++i) {
-          ok = mbar_wait(&ctl.ds_full[i], t & 1, wc, 0xb5);
-          if (!ok) break;
+        if (!mbar_wait(&ctl.ds_full, t & 1, wc, 0xb5)) break;  // dS is written, dP read
+        tc_fence_after();
+        if (t + 1 < steps) {
+          if (!mbar_wait(&ctl.v_full[(t + 1) % kShort], ((t + 1) / kShort) & 1, wc, 0xbc)) break;
           tc_fence_after();
+          issue_dp(t + 1);
+        }
+        const uint64_t bm = desc_local(desc_advance(mk0, (t % kDeep) * kTileB));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(t_dq, tmem + i * 64 + kk * 8, desc_advance(mk0, cur + i * 8192 + kk * 2048), idesc_g,
-                    (t | i | kk) != 0);
-          umma_commit(&ctl.mm_done[i]);
-          if (i == 1) umma_commit(&ctl.kv_empty[t % kStages]);
-          if (t + 1 < steps) {
-            if (i == 0) ok = mbar_wait(&ctl.kv_full[(t + 1) % kStages], ((t + 1) / kStages) & 1, wc, 0xb3);
-            if (!ok) break;
-            tc_fence_after();
-            issue_ab(tmem + 128 + i * 64, dd0, desc_advance(dv0, nxt), i);
-            ok = mbar_wait(&ctl.mm_done[i], t & 1, wc, 0xb6);  // the product that reads dS has finished
-            if (!ok) break;
-            tc_fence_after();
-            issue_ab(tmem + i * 64, dq0, desc_advance(dk0, nxt), i);
-            umma_commit(&ctl.s_full[i]);
-          }
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          umma_ts_lead(lead, t_dq, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bm, kk * 2048),
+                       idesc_g, (t | kk) != 0);
+        umma_commit_lead(lead, &ctl.dq_done);
+        umma_commit_lead(lead, &ctl.k_empty[t % kDeep]);
+        if (t + 2 < steps) {
+          if (!mbar_wait(&ctl.k_full[(t + 2) % kDeep], ((t + 2) / kDeep) & 1, wc, 0xb3) ||
+              !mbar_wait(&ctl.dq_done, t & 1, wc, 0xb6))  // dS of this buffer has been read
+            break;
+          tc_fence_after();
+          issue_s(t + 2);
         }
       }
     }
   } else {
-    // ------------------------------------------------ softmax warps: thread = query row
-    const int hf = warp >> 2;              // which half of the key tile
+    // ------------------------------------------------ softmax warps: thread = query row, 32 keys
+    const int cg = warp >> 2;              // which quarter of the key tile
     const int r = (warp & 3) * 32 + lane;  // query row
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + hf * 64 + lane_base, t_dp = tmem + 128 + hf * 64 + lane_base;
     const int row = row0 + r, pos = w.off + row;
     const int end = min(window_end(w, pos), len), low = window_low(w, window_end(w, pos));
     const int pos1 = min(min(w.off + row0 + kRows, w.off + w.N), len) - 1;
-    const int all_end = min(window_end(w, w.off + row0), len);
+    const int all_end = pos1 - w.off - row0 < kRows - 1 ? 0 : min(window_end(w, w.off + row0), len);
     const int all_low = window_low(w, window_end(w, max(pos1, 0)));
     const size_t at = ((size_t)b * w.heads + h) * n_pad + row;  // row < n_pad
     const float nl = nlse[at], nd = ndelta[at];
@@ -639,76 +734,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2 = pk2(sl, sl), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
     bool ok = true;
     for (int t = 0; t < steps; ++t) {
-      const int key0 = tile_of(t) * kRows + hf * 64;
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[hf], t & 1, wc, 0xb8));
+      const int key0 = tile_of(t) * kRows + cg * 32;
+      const uint32_t my_s = tmem + (t & 1) * 128 + cg * 32 + lane_base, my_dp = t_dp + cg * 32 + lane_base;
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[t & 1], (t >> 1) & 1, wc, 0xb8));
       if (!ok) break;
       tc_fence_after();
-      const bool masked = key0 + 64 > all_end || (key0 < all_low && key0 + 64 > w.sinks) || pos1 - w.off - row0 < kRows - 1;
-      uint32_t vis[2] = {~0u, ~0u};
-      if (masked) {
-        vis[0] = live ? visible_bits(key0, low, end, w.sinks) : 0u;
-        vis[1] = live ? visible_bits(key0 + 32, low, end, w.sinks) : 0u;
-      }
+      // (a tile with dead rows is always masked)
+      const bool masked = key0 + 32 > all_end || (key0 < all_low && key0 + 32 > w.sinks);
+      uint32_t buf[32], pk[16];
+      tmem_ld32(my_s, buf);
+      tmem_ld_wait();
+      tmem_tie(buf);
+      float p[32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t s[32], d[32], pk[16];
-        tmem_ld32(t_s + c * 32, s);
-        tmem_ld32(t_dp + c * 32, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x0, x1, g0, g1;
-          up2(fma2(pk2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sl2, nl2), x0, x1);
-          const uint64_t p = pk2(ex2(x0), ex2(x1));
-          up2(mul2(add2(pk2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), nd2), p), g0, g1);
-          if (masked) {
-            if (!(vis[c] & (1u << (2 * i)))) g0 = 0.f;
-            if (!(vis[c] & (2u << (2 * i)))) g1 = 0.f;
-          }
-          pk[i] = f2_to_bf2(g0, g1);
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t x = fma2(pk2(__uint_as_float(buf[i]), __uint_as_float(buf[i + 1])), sl2, nl2);
+        if (((i >> 1) & 7) >= 8 - kEmuPairs) {
+          exp2_pair(x, p[i], p[i + 1]);
+        } else {
+          up2(x, p[i], p[i + 1]);
+          p[i] = ex2(p[i]);
+          p[i + 1] = ex2(p[i + 1]);
         }
-        tmem_st16(t_s + c * 16, pk);
       }
-      tmem_st_wait();
-      if (key0 + 64 > len && len < w.N_keys) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dp_full, t & 1, wc, 0xb9));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(my_dp, buf);
+      tmem_ld_wait();
+      tmem_tie(buf);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const uint64_t d = add2(pk2(__uint_as_float(buf[i]), __uint_as_float(buf[i + 1])), nd2);
+        up2(mul2(d, pk2(p[i], p[i + 1])), p[i], p[i + 1]);
+      }
+      if (masked) {
+        const uint32_t vis = live ? visible_bits(key0, low, end, w.sinks) : 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(vis & (1u << i))) p[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = f2_to_bf2(p[2 * i], p[2 * i + 1]);
+      tmem_st16(my_s, pk);
+      if (key0 + 32 > len && len < w.N_keys) {
         // padding rows of K meet dS = 0: zero them, whatever they hold
-        if (r < 64 && key0 + r >= len) {
-          uint8_t* base = k_s + (t % kStages) * kTileB;
+        if (r < 32 && key0 + r >= len) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(base + (c >> 3) * kHalf + sw128_off(hf * 64 + r, c & 7)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(k_s + (t % kDeep) * kTileB + (c >> 3) * kHalf + sw128_off(cg * 32 + r, c & 7)) =
+                make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&ctl.ds_full[hf]);
+      mbar_arrive(&ctl.ds_full);
     }
-    // ---------------- epilogue: warpgroup 0 writes columns [0, 64), 1 the rest
-    if (steps > 0 && ok) {
-      ok = mbar_wait(&ctl.mm_done[0], (steps - 1) & 1, wc, 0xb9) && mbar_wait(&ctl.mm_done[1], (steps - 1) & 1, wc, 0xba);
-      ok = __all_sync(0xffffffffu, ok);
-    }
+    // ---------------- epilogue: each quarter writes its 32 columns
+    if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dq_done, (steps - 1) & 1, wc, 0xba));
     if (ok) {
       tc_fence_after();
-      __nv_bfloat16* dst = dq + (((size_t)b * w.N + row) * w.heads + h) * kD + hf * 64;
+      __nv_bfloat16* dst = dq + (((size_t)b * w.N + row) * w.heads + h) * kD + cg * 32;
+      uint32_t o[32];
+      if (steps > 0) {
+        tmem_ld32(t_dq + lane_base + cg * 32, o);
+        tmem_ld_wait();
+        tmem_tie(o);
+      }
+      if (row < w.N) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t o[32];
-        if (steps > 0) {
-          tmem_ld32(t_dq + lane_base + hf * 64 + c * 32, o);
-          tmem_ld_wait();
-        }
-        if (row < w.N) {
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = live && steps > 0 ? f2_to_bf2(scale * __uint_as_float(o[8 * i + 2 * e]),
-                                                   scale * __uint_as_float(o[8 * i + 2 * e + 1]))
-                                       : 0u;
-            *reinterpret_cast<uint4*>(dst + c * 32 + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            v[e] = live && steps > 0 ? f2_to_bf2(scale * __uint_as_float(o[8 * i + 2 * e]),
+                                                 scale * __uint_as_float(o[8 * i + 2 * e + 1]))
+                                     : 0u;
+          *reinterpret_cast<uint4*>(dst + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
     }
@@ -716,16 +819,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
-    if (*wc.abort_flag && steps > 0) {
-      mbar_drain(&ctl.mm_done[0], (steps - 1) & 1);
-      mbar_drain(&ctl.mm_done[1], (steps - 1) & 1);
-    }
+    if (*wc.abort_flag && steps > 0) mbar_drain(&ctl.dq_done, (steps - 1) & 1);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-constexpr size_t kBwdSmem = 1024 + (2 + 2 * kStages) * (size_t)kTileB;
+constexpr size_t kSmemMax = 227 * 1024;
+static_assert(kDkvSmem + sizeof(DkvCtl) <= kSmemMax && kDqSmem + sizeof(DqCtl) <= kSmemMax, "shared memory");
 
 // A key tile is left whole while there are two CTAs for every SM; otherwise its
 // steps are cut so that there are, down to four steps each.  The sinks' tiles,
@@ -797,8 +898,8 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
       !make_tmap_bf16_3d(&tv, c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows))
     return fail(SANA_ERR_CUDA, "windowed anchor backward: cuTensorMapEncodeTiled failed");
   once_per_context(kAttrWindowBwd, [] {
-    cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
-    cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBwdSmem);
+    cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDkvSmem + sizeof(DkvCtl)));
+    cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDqSmem + sizeof(DqCtl)));
   });
   using bf = __nv_bfloat16;
   const long long rows = (long long)c.B * n_pad * c.heads;
@@ -814,7 +915,7 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
   int* sw = status_word();
   const DkvPlan p = dkv_plan(c);
   const int items = dkv_items(p);
-  window_dkv_kernel<<<dim3(items, c.kv_heads, c.B), kThreads, kBwdSmem, st>>>(
+  window_dkv_kernel<<<dim3(items, c.kv_heads, c.B), kThreads, kDkvSmem + sizeof(DkvCtl), st>>>(
       tq, td, tk, tv, w, p, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dk, (bf*)dv, sw);
   if (sana_status e = check_launch("window_dkv_kernel")) return e;
   const int split = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.win_parts > 1 ? p.tiles - p.sink_tiles : 0);
@@ -822,7 +923,7 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
     window_join_kernel<<<dim3(2 * split, c.kv_heads, c.B), 512, 0, st>>>(m.part, w, p, items, (bf*)dk, (bf*)dv);
     if (sana_status e = check_launch("window_join_kernel")) return e;
   }
-  window_dq_kernel<<<dim3((c.N + kRows - 1) / kRows, c.heads, c.B), kThreads, kBwdSmem, st>>>(
+  window_dq_kernel<<<dim3((c.N + kRows - 1) / kRows, c.heads, c.B), kThreads, kDqSmem + sizeof(DqCtl), st>>>(
       tq, td, tk, tv, w, sl, c.scale, n_pad, m.nlse, m.ndelta, (bf*)dq, sw);
   return check_launch("window_dq_kernel");
 }
