@@ -13,10 +13,13 @@
 //   dw = sum_rows g x r,   dx = r (w g - x r^2 mean_d(w g x)).
 //
 // Bound by HBM: each element is read once and written once (the gradient reads
-// x and dy and writes dx); the table adds 8 bytes per pair and token.  A lane
-// holds 8 consecutive elements of a row (16-byte accesses), a row sits in
-// head_dim / 8 neighbouring lanes (the partner in the half layout is a shuffle
-// away), and a warp walks the heads of one token, four row groups in flight.
+// x and dy and writes dx); the table adds 8 bytes per pair and token.  What holds
+// it from there is the instruction count, so arithmetic runs in packed pairs and
+// a warp walks all heads of one token, queries and then keys, with one lookup of
+// the angles.  A lane holds 8 consecutive elements of a row (16-byte accesses) and
+// a row sits in head_dim / 8 neighbouring lanes (the partner in the half layout
+// is a shuffle away), several row groups in flight.
+#include "f32x2.cuh"
 #include "pdl.cuh"
 #include "rope_dev.cuh"
 #include "sana_common.cuh"
@@ -25,9 +28,16 @@
 namespace sana {
 namespace {
 
-constexpr int kWarps = 8;      // warps per CTA
+constexpr int kWarps = 4;      // warps per CTA: a warp does one token, short CTAs drain evenly
+constexpr int kWarpsBwd = 8;   // warps per CTA of the gradient, which is persistent
 constexpr int kUnroll = 4;     // row groups a warp has in flight (forward)
-constexpr int kUnrollBwd = 2;  // the same for the gradient, which loads two tensors
+// The same for the gradient, which loads two tensors (fp32 rows are twice as wide).
+template <class T>
+constexpr int kUnrollBwd = sizeof(T) == 2 ? 4 : 2;
+// CTAs on an SM that the forward's registers are held to (bf16: 480p grid, 16 heads
+// of 128: 87 us against 91 us unheld; fp32 rows need the registers).
+template <class T>
+constexpr int kResident = sizeof(T) == 2 ? 7 : 4;
 
 // Eight consecutive elements of a row as loaded.
 template <class T>
@@ -46,17 +56,22 @@ struct Vec8<__nv_bfloat16> {
     for (int i = 0; i < 4; ++i) o.r[i] = __shfl_sync(0xffffffffu, r[i], src);
     return o;
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = bf2_to_f2(r[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
+      f[i] = pk2(v.x, v.y);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(f2_to_bf2(f[0], f[1]), f2_to_bf2(f[2], f[3]),
-                                                  f2_to_bf2(f[4], f[5]), f2_to_bf2(f[6], f[7])));
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const uint64_t (&f)[4]) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      up2(f[i], a, b);
+      o[i] = f2_to_bf2(a, b);
+    }
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(o[0], o[1], o[2], o[3]));
   }
 };
 template <>
@@ -78,13 +93,16 @@ struct Vec8<float> {
     for (int i = 0; i < 8; ++i) o.r[i] = __shfl_sync(0xffffffffu, r[i], src);
     return o;
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = r[i];
+    for (int i = 0; i < 4; ++i) f[i] = pk2(r[2 * i], r[2 * i + 1]);
   }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  static __device__ __forceinline__ void store(float* p, const uint64_t (&f)[4]) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) up2(f[i], o[2 * i], o[2 * i + 1]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(o[0], o[1], o[2], o[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(o[4], o[5], o[6], o[7]));
   }
 };
 
@@ -149,20 +167,24 @@ struct Turn {
     if (HALF) return second != back ? s[i % kP] : -s[i % kP];
     return ((i & 1) != 0) != back ? s[(i >> 1) % kP] : -s[(i >> 1) % kP];
   }
-  // The pair partners of v (zeros where the lane is not rotated, so that an
-  // infinity there meets no 0 * inf).
+  // a * x + b * x' for the row of v, x its elements in pairs (partners count as
+  // zero where the lane is not rotated, so that an infinity there meets no 0 * inf).
   template <class T>
-  __device__ __forceinline__ void partners(const Vec8<T>& v, const float (&x)[8], float (&xp)[8]) const {
+  __device__ __forceinline__ void apply(const Vec8<T>& v, const uint64_t (&x)[4], const uint64_t (&a)[4],
+                                        const uint64_t (&b)[4], uint64_t (&y)[4]) const {
+    uint64_t xp[4];
     if (HALF) {
       v.from_lane(partner).get(xp);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xp[i] = x[i ^ 1];
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        up2(x[i], lo, hi);
+        xp[i] = pk2(hi, lo);
+      }
     }
-    if (!on) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) xp[i] = 0.f;
-    }
+    for (int i = 0; i < 4; ++i) y[i] = fma2(b[i], on ? xp[i] : 0ull, mul2(a[i], x[i]));
   }
 };
 
@@ -173,84 +195,114 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void load_w(const float* w, int col, float (&f)[8]) {
+// Sums of u and v over a row's LPR lanes: neighbours share the work after the
+// first step (one shuffle for both), and swap the results at the end.
+template <int LPR>
+__device__ __forceinline__ void row_sum2(float& u, float& v, int lane) {
+  const bool odd = lane & 1;
+  float mine = odd ? v : u;
+  mine += __shfl_xor_sync(0xffffffffu, odd ? u : v, 1);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = w ? __ldg(w + col + i) : 1.f;
+  for (int m = 2; m < LPR; m <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, m);
+  const float other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  u = odd ? other : mine;
+  v = odd ? mine : other;
+}
+__device__ __forceinline__ float sum_squares(const uint64_t (&f)[4]) {
+  uint64_t s = mul2(f[0], f[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(f[i], f[i], s);
+  float a, b;
+  up2(s, a, b);
+  return a + b;
+}
+__device__ __forceinline__ void load_w(const float* w, int col, uint64_t (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f[i] = w ? pk2(__ldg(w + col + 2 * i), __ldg(w + col + 2 * i + 1)) : pk2(1.f, 1.f);
 }
 
-// One warp: one token and `per_warp` of its query heads, or of its key heads.
+// One warp: one token and `per_warp` row groups of it (a group: 32 / LPR heads),
+// numbered through its queries and then its keys.
 template <class T, int LPR, bool HALF, bool NORM>
-__global__ void __launch_bounds__(32 * kWarps)
-    qk_norm_rope_kernel(const QkTensors a, const RotaryDev rt, int chunks_q, int chunks_k,
-                        int per_warp, float eps, float q_mul, int* status) {
+__global__ void __launch_bounds__(32 * kWarps, kResident<T>)
+    qk_norm_rope_kernel(const QkTensors a, const RotaryDev rt, int chunks, int per_warp, float eps,
+                        float q_mul, int* status) {
   constexpr int D = LPR * 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31;
   const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int chunks = chunks_q + chunks_k;
-  const long long token = task / chunks;
+  const long long token = chunks == 1 ? task : task / chunks;
   if (token >= (long long)a.B * a.N) return;
-  const int chunk = (int)(task - token * chunks);
-  const bool is_q = chunk < chunks_q;
-  const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-  const int heads = is_q ? a.heads : a.kv_heads;
-  const int h0 = (is_q ? chunk : chunk - chunks_q) * per_warp;
-  const int h1 = min(heads, h0 + per_warp);
-  const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride);
-  T* y = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D;
+  const int chunk = chunks == 1 ? 0 : (int)(task - token * chunks);
+  const int b = (int)((unsigned)token / (unsigned)a.N), n = (int)token - b * a.N;
+  const int groups_q = (a.heads + RPW - 1) / RPW, groups_k = (a.kv_heads + RPW - 1) / RPW;
+  const int g0 = chunk * per_warp, g1 = min(groups_q + groups_k, g0 + per_warp);
   const int col = (lane % LPR) * 8, sub_row = lane / LPR;
-
-  // the rows' loads start before the table is looked up
-  Vec8<T> raw[kUnroll];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int hr = h + u * RPW + sub_row;
-      if (hr < h1) raw[u].load(x + (size_t)hr * D + col);
-      else raw[u].zero();
-    }
-  };
-  load(h0);
 
   Turn<LPR, HALF> turn;
   turn.init(rt, lane);
-  turn.fetch(rt, b, n, lane, status);
-  float ca[8], cb[8];
-  {
-    const float m = is_q ? q_mul : 1.f;
-    const float* w = is_q ? a.wq : a.wk;
-    float wo[8], wp[8];
-    if (NORM) {
-      load_w(w, col, wo);
-      load_w(w, HALF ? (turn.partner % LPR) * 8 : col, wp);
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ca[i] = m * turn.own(i) * (NORM ? wo[i] : 1.f);
-      cb[i] = m * turn.other(i, false) * (NORM ? (HALF ? wp[i] : wp[i ^ 1]) : 1.f);
-    }
-  }
-  for (int h = h0; h < h1; h += kUnroll * RPW) {
-    if (h > h0) load(h);
+  for (int side = 0; side < 2; ++side) {
+    const bool is_q = side == 0;
+    const int heads = is_q ? a.heads : a.kv_heads;
+    const int lo = is_q ? g0 : max(g0 - groups_q, 0), hi = is_q ? min(g1, groups_q) : g1 - groups_q;
+    if (lo < hi) {
+      const int h1 = min(heads, hi * RPW);
+      const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride) + col;
+      T* y = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D + col;
+      Vec8<T> raw[kUnroll];
+      auto load = [&](int h) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (h + u * RPW >= h1) break;  // warp-uniform
-      const int hr = h + u * RPW + sub_row;
-      float f[8], fp[8];
-      raw[u].get(f);
-      turn.partners(raw[u], f, fp);
-      float r = 1.f;
-      if (NORM) {
-        float ss = 0.f;
+        for (int u = 0; u < kUnroll; ++u) {
+          const int hr = h + u * RPW + sub_row;
+          if (hr < h1) raw[u].load(x + (size_t)hr * D);
+          else raw[u].zero();
+        }
+      };
+      load(lo * RPW);  // the rows' loads start before the table is looked up
+      if (is_q || g0 >= groups_q) turn.fetch(rt, b, n, lane, status);
+      uint64_t ca[4], cb[4];
+      {
+        const float m = is_q ? q_mul : 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-        r = 1.f / sqrtf(row_sum<LPR>(ss) * (1.f / D) + eps);
+        for (int i = 0; i < 4; ++i) {
+          ca[i] = pk2(m * turn.own(2 * i), m * turn.own(2 * i + 1));
+          cb[i] = pk2(m * turn.other(2 * i, false), m * turn.other(2 * i + 1, false));
+        }
+        const float* w = is_q ? a.wq : a.wk;
+        if (NORM && w) {
+          uint64_t wo[4], wp[4];
+          load_w(w, col, wo);
+          if (HALF) load_w(w, (turn.partner % LPR) * 8, wp);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!HALF) {
+              float p0, p1;
+              up2(wo[i], p0, p1);
+              wp[i] = pk2(p1, p0);
+            }
+            ca[i] = mul2(ca[i], wo[i]);
+            cb[i] = mul2(cb[i], wp[i]);
+          }
+        }
       }
+      for (int h = lo * RPW; h < h1; h += kUnroll * RPW) {
+        if (h > lo * RPW) load(h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = fmaf(cb[i], fp[i], ca[i] * f[i]);
-        if (NORM) f[i] *= r;
+        for (int u = 0; u < kUnroll; ++u) {
+          if (h + u * RPW >= h1) break;  // warp-uniform
+          const int hr = h + u * RPW + sub_row;
+          uint64_t f[4], o[4];
+          raw[u].get(f);
+          turn.apply(raw[u], f, ca, cb, o);
+          if (NORM) {
+            const float r = rsqrtf(row_sum<LPR>(sum_squares(f)) * (1.f / D) + eps);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = mul2(o[i], pk2(r, r));
+          }
+          if (hr < h1) Vec8<T>::store(y + (size_t)hr * D, o);
+        }
       }
-      if (hr < h1) Vec8<T>::store(y + (size_t)hr * D + col, f);
     }
   }
 }
@@ -261,67 +313,76 @@ __global__ void __launch_bounds__(32 * kWarps)
 // and the CTA's sums written out, to be added in CTA order by the next kernel:
 // the summation order depends on the shape alone.
 template <class T, int LPR, bool HALF>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+__global__ void __launch_bounds__(32 * kWarpsBwd, 2)
     qk_norm_rope_bwd_kernel(const QkTensors a, const RotaryDev rt, float eps, float q_mul,
                             float* __restrict__ dw_part, int* status) {
   constexpr int D = LPR * 8, RPW = 32 / LPR;
-  __shared__ float red[kWarps][2][D];
+  __shared__ float red[kWarpsBwd][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = (lane % LPR) * 8, sub_row = lane / LPR;
   Turn<LPR, HALF> turn;
   turn.init(rt, lane);
-  float dw[2][8] = {};
+  uint64_t dw[2][4] = {};
   const long long tokens = (long long)a.B * a.N;
-  for (long long token = (long long)blockIdx.x * kWarps + warp; token < tokens;
-       token += (long long)gridDim.x * kWarps) {
-    const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
+  for (long long token = (long long)blockIdx.x * kWarpsBwd + warp; token < tokens;
+       token += (long long)gridDim.x * kWarpsBwd) {
+    const int b = (int)((unsigned)token / (unsigned)a.N), n = (int)token - b * a.N;
     turn.fetch(rt, b, n, lane, status);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const bool is_q = side == 0;
       const int heads = is_q ? a.heads : a.kv_heads;
-      const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride);
-      const T* dy = static_cast<const T*>(is_q ? a.dq_out : a.dk_out) + (size_t)token * heads * D;
-      T* dx = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D;
+      const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride) + col;
+      const T* dy = static_cast<const T*>(is_q ? a.dq_out : a.dk_out) + (size_t)token * heads * D + col;
+      T* dx = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D + col;
       const float m = is_q ? q_mul : 1.f;
-      float w[8];
-      load_w(is_q ? a.wq : a.wk, col, w);
-      for (int h = 0; h < heads; h += kUnrollBwd * RPW) {
-        Vec8<T> rx[kUnrollBwd], rg[kUnrollBwd];
+      uint64_t ca[4], cb[4], w[4];
 #pragma unroll
-        for (int u = 0; u < kUnrollBwd; ++u) {
+      for (int i = 0; i < 4; ++i) {
+        ca[i] = pk2(m * turn.own(2 * i), m * turn.own(2 * i + 1));
+        cb[i] = pk2(m * turn.other(2 * i, true), m * turn.other(2 * i + 1, true));
+      }
+      load_w(is_q ? a.wq : a.wk, col, w);
+      for (int h = 0; h < heads; h += kUnrollBwd<T> * RPW) {
+        Vec8<T> rx[kUnrollBwd<T>], rg[kUnrollBwd<T>];
+#pragma unroll
+        for (int u = 0; u < kUnrollBwd<T>; ++u) {
           const int hr = h + u * RPW + sub_row;
           if (hr < heads) {
-            rx[u].load(x + (size_t)hr * D + col);
-            rg[u].load(dy + (size_t)hr * D + col);
+            rx[u].load(x + (size_t)hr * D);
+            rg[u].load(dy + (size_t)hr * D);
           } else {
             rx[u].zero();
             rg[u].zero();
           }
         }
 #pragma unroll
-        for (int u = 0; u < kUnrollBwd; ++u) {
+        for (int u = 0; u < kUnrollBwd<T>; ++u) {
           if (h + u * RPW >= heads) break;  // warp-uniform
           const int hr = h + u * RPW + sub_row;
-          float f[8], g[8], gp[8];
+          uint64_t f[4], d[4], g[4];
           rx[u].get(f);
-          rg[u].get(g);
-          turn.partners(rg[u], g, gp);
-          float ss = 0.f, dot = 0.f;
+          rg[u].get(d);
+          turn.apply(rg[u], d, ca, cb, g);
+          float ss = sum_squares(f), dot, t1;
+          uint64_t gf = 0, gw[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            g[i] = m * fmaf(turn.other(i, true), gp[i], turn.own(i) * g[i]);
-            ss = fmaf(f[i], f[i], ss);
-            dot = fmaf(g[i] * w[i], f[i], dot);
+          for (int i = 0; i < 4; ++i) {
+            gw[i] = mul2(g[i], w[i]);
+            gf = fma2(gw[i], f[i], gf);
           }
-          const float r = 1.f / sqrtf(row_sum<LPR>(ss) * (1.f / D) + eps);
-          const float k3 = r * r * (row_sum<LPR>(dot) * (1.f / D));
+          up2(gf, dot, t1);
+          dot += t1;
+          row_sum2<LPR>(ss, dot, lane);
+          const float r = rsqrtf(ss * (1.f / D) + eps);
+          const float k3 = -r * r * r * (dot * (1.f / D));
+          const uint64_t r2 = pk2(r, r), k32 = pk2(k3, k3);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            dw[side][i] = fmaf(g[i], f[i] * r, dw[side][i]);
-            g[i] = r * fmaf(-k3, f[i], g[i] * w[i]);
+          for (int i = 0; i < 4; ++i) {
+            dw[side][i] = fma2(g[i], mul2(f[i], r2), dw[side][i]);
+            g[i] = fma2(k32, f[i], mul2(r2, gw[i]));
           }
-          if (hr < heads) Vec8<T>::store(dx + (size_t)hr * D + col, g);
+          if (hr < heads) Vec8<T>::store(dx + (size_t)hr * D, g);
         }
       }
     }
@@ -331,16 +392,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
   for (int side = 0; side < 2; ++side)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float v = dw[side][i];
+      float v, v1;
+      up2(dw[side][i >> 1], v, v1);
+      if (i & 1) v = v1;
 #pragma unroll
       for (int mk = LPR; mk < 32; mk <<= 1) v += __shfl_xor_sync(0xffffffffu, v, mk);
       if (sub_row == 0) red[warp][side][col + i] = v;
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarpsBwd) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += red[k][i / D][i % D];
+    for (int k = 0; k < kWarpsBwd; ++k) v += red[k][i / D][i % D];
     dw_part[(size_t)blockIdx.x * 2 * D + i] = v;
   }
 }
@@ -385,7 +448,7 @@ __global__ void rotary_table_kernel(float2* table, int max_positions, int pairs,
 
 // Grid of the gradient kernel: two CTAs per SM, fewer for few tokens.
 int bwd_ctas(long long tokens) {
-  const long long c = (tokens + kWarps - 1) / kWarps;
+  const long long c = (tokens + kWarpsBwd - 1) / kWarpsBwd;
   return (int)(c < 2 * kNumSMs ? c : 2 * kNumSMs);
 }
 
@@ -397,18 +460,17 @@ void launch_fwd(const QkTensors& a, const RotaryDev& rt, bool norm, float eps, f
   // all of them for long inputs (the table lookup is then shared by all
   // heads), one row group each for a decoding step (latency).
   const long long tokens = (long long)a.B * a.N;
-  const int groups_q = (a.heads + RPW - 1) / RPW, groups_k = (a.kv_heads + RPW - 1) / RPW;
-  long long want = (16 * kNumSMs + tokens - 1) / tokens;  // warps per token
-  int per = (int)((groups_q + groups_k + want - 1) / want);
+  const int groups = (a.heads + RPW - 1) / RPW + (a.kv_heads + RPW - 1) / RPW;
+  const long long want = (16 * kNumSMs + tokens - 1) / tokens;  // warps per token
+  int per = (int)((groups + want - 1) / want);
   if (per < 1) per = 1;
-  const int cq = (groups_q + per - 1) / per, ck = (groups_k + per - 1) / per;
-  const long long tasks = tokens * (cq + ck);
-  const dim3 grid((unsigned)((tasks + kWarps - 1) / kWarps));
+  const int chunks = (groups + per - 1) / per;
+  const dim3 grid((unsigned)((tokens * chunks + kWarps - 1) / kWarps));
   int* sw = status_word();
   if (norm)
-    qk_norm_rope_kernel<T, LPR, HALF, true><<<grid, 32 * kWarps, 0, st>>>(a, rt, cq, ck, per * RPW, eps, q_mul, sw);
+    qk_norm_rope_kernel<T, LPR, HALF, true><<<grid, 32 * kWarps, 0, st>>>(a, rt, chunks, per, eps, q_mul, sw);
   else
-    qk_norm_rope_kernel<T, LPR, HALF, false><<<grid, 32 * kWarps, 0, st>>>(a, rt, cq, ck, per * RPW, eps, q_mul, sw);
+    qk_norm_rope_kernel<T, LPR, HALF, false><<<grid, 32 * kWarps, 0, st>>>(a, rt, chunks, per, eps, q_mul, sw);
 }
 
 template <class T, int LPR, bool HALF>
@@ -416,7 +478,7 @@ void launch_bwd(const QkTensors& a, const RotaryDev& rt, float eps, float q_mul,
                 float* dwk, float* ws, cudaStream_t st) {
   const int ctas = bwd_ctas((long long)a.B * a.N);
   if (ctas)  // no tokens: the sums over nothing below are zeros
-    qk_norm_rope_bwd_kernel<T, LPR, HALF><<<ctas, 32 * kWarps, 0, st>>>(a, rt, eps, q_mul, ws, status_word());
+    qk_norm_rope_bwd_kernel<T, LPR, HALF><<<ctas, 32 * kWarpsBwd, 0, st>>>(a, rt, eps, q_mul, ws, status_word());
   qk_dw_reduce_kernel<<<(2 * LPR * 8 + 31) / 32, 1024, 0, st>>>(ws, ctas, LPR * 8, dwq, dwk);
 }
 

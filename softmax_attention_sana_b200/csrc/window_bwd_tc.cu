@@ -53,12 +53,6 @@ constexpr int kWarpProd = 16, kWarpMma = 17;
 constexpr int kEmuPairs = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // 2^x for two x <= 0 (or a little above) on the FMA pipe: n = round(x) in the low
 // mantissa bits of x + 1.5 * 2^23, a cubic on [-1/2, 1/2] (7.5e-5 relative), n
 // added to the exponent.  Below -126 counts as -126: nothing in bf16 or beside 1.
