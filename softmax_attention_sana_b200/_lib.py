@@ -532,24 +532,46 @@ class Rotary:
                                         None if sc is None else ctypes.byref(sc), _ptr(self.table),
                                         _stream()))
         self.struct = RotaryStruct(self.table.data_ptr(), max_positions, rotary_dim, _LAYOUTS[layout])
+        self.pointer = ctypes.pointer(self.struct)
 
 
 def _same_device(first, *others):
+    at = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != at:
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+
+
+def _call_on(t, fn, *args):
+    """fn(*args, stream) on t's device and its current stream, checked."""
+    index = t.get_device()
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != SANA_OK:
+        raise SanaError(status, last_error())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _token_stride(t, name, width):
     """Elements between the tokens of a (B, N, width) tensor whose rows are contiguous and whose
     sequences follow each other at the same stride (a slice of a packed projection is one)."""
-    if not t.is_cuda or t.dim() != 3 or t.shape[2] != width or (width > 1 and t.stride(2) != 1):
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor (B, N, {width})")
+    B, N, C = t.shape
+    seq, step, unit = t.stride()
+    if C != width or (unit != 1 and C > 1):
         raise ValueError(f"{name} must be a CUDA tensor (B, N, {width}) with contiguous rows")
-    B, N = t.shape[:2]
-    step = t.stride(1) if N > 1 else t.stride(0) if B > 1 else width
-    if t.numel() and N > 1 and B > 1 and t.stride(0) != N * step:
-        raise ValueError(f"{name}: sequences must follow each other at the tokens' stride")
-    return step if t.numel() else width
+    if N > 1:
+        if B > 1 and seq != N * step:
+            raise ValueError(f"{name}: sequences must follow each other at the tokens' stride")
+        return step if B else width
+    return seq if B > 1 and N else width
 
 
 def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
@@ -564,23 +586,20 @@ def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
         raise ValueError("q and k must have one dtype and the same (B, N)")
     s = QkShape(B, N, heads, kv_heads, D, _token_stride(q, "q", C),
                 0 if k is None else _token_stride(k, "k", kv_heads * D))
-    at = QkPositions(positions=None, offset=offset)
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (B, N) or
+                                  not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 tensor (B, N)")
     if isinstance(rotary, Rope):
         if grid is None:
             raise ValueError("a Rope needs the tokens' grid=(T, H, W)")
-        at.rope, (at.T, at.H, at.W) = ctypes.pointer(rotary.struct), grid
-        if rotary.tables.device != q.device:
-            raise ValueError("the rotary tables are on another device than q")
+        at = QkPositions(None, ctypes.pointer(rotary.struct), *grid, _addr(positions), offset)
+        table = rotary.tables
     else:
         if grid is not None:
             raise ValueError("grid goes with a Rope")
-        at.rotary = ctypes.pointer(rotary.struct)
-        _same_device(q, rotary.table)
-    if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape != (B, N) or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous int32 tensor (B, N)")
-        at.positions = positions.data_ptr()
-    _same_device(q, k, positions)
+        at = QkPositions(rotary.pointer, None, 0, 0, 0, _addr(positions), offset)
+        table = rotary.table
+    _same_device(q, k, positions, table)
     return s, at
 
 
@@ -595,7 +614,7 @@ def _norm_weight(w, name, q, D):
 
 def _out_like(out, name, q, width):
     if out is None:
-        return torch.empty(*q.shape[:2], width, dtype=q.dtype, device=q.device)
+        return q.new_empty((*q.shape[:2], width))
     _need(out, name)
     if out.dtype != q.dtype or tuple(out.shape) != (*q.shape[:2], width):
         raise ValueError(f"{name} must be {q.dtype} {(*q.shape[:2], width)}")
@@ -611,10 +630,8 @@ def rotary_apply(q, k, rotary, heads, kv_heads, positions=None, offset=0, grid=N
     s, at = _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid)
     q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
     k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
-    with torch.cuda.device(q.device):
-        check(lib.sana_rotary_apply(ctypes.byref(s), _dtype_code(q), ctypes.byref(at),
-                                    int(bool(inverse)), _ptr(q), _ptr(k), q_mul, _ptr(q_out),
-                                    _ptr(k_out), _stream()))
+    _call_on(q, lib.sana_rotary_apply, s, _dtype_code(q), at, int(bool(inverse)), q.data_ptr(),
+             _addr(k), q_mul, q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
 
 
@@ -627,10 +644,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, rotary, heads, kv_heads, positions=No
     _norm_weight(k_weight, "k_weight", q, s.head_dim)
     q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
     k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
-    with torch.cuda.device(q.device):
-        check(lib.sana_qk_norm_rope(ctypes.byref(s), _dtype_code(q), ctypes.byref(at), _ptr(q),
-                                    _ptr(k), _ptr(q_weight), _ptr(k_weight), eps, q_mul,
-                                    _ptr(q_out), _ptr(k_out), _stream()))
+    _call_on(q, lib.sana_qk_norm_rope, s, _dtype_code(q), at, q.data_ptr(), _addr(k),
+             _addr(q_weight), _addr(k_weight), eps, q_mul, q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
 
 
@@ -658,11 +673,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv
     if ws is None:
         ws = _ws(lib.sana_qk_norm_rope_bwd_workspace_size(ctypes.byref(s)), q.device)
     _same_device(q, ws)
-    with torch.cuda.device(q.device):
-        check(lib.sana_qk_norm_rope_bwd(
-            ctypes.byref(s), _dtype_code(q), ctypes.byref(at), _ptr(q), _ptr(k), _ptr(q_weight),
-            _ptr(k_weight), eps, q_mul, _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dwq),
-            _ptr(dwk), _ptr(ws), ws.numel(), _stream()))
+    _call_on(q, lib.sana_qk_norm_rope_bwd, s, _dtype_code(q), at, q.data_ptr(), _addr(k),
+             _addr(q_weight), _addr(k_weight), eps, q_mul, dq_out.data_ptr(), _addr(dk_out),
+             dq.data_ptr(), _addr(dk), dwq.data_ptr(), _addr(dwk), ws.data_ptr(), ws.numel())
     return dq, dk, dwq, dwk
 
 
@@ -708,9 +721,8 @@ def window_anchor_fwd(q, k, v, gate, heads, kv_heads, window, sinks=0, block=1, 
         _same_device(q, lse)
         if lse.dtype != torch.float32 or lse.shape != (s.B, heads, s.N):
             raise ValueError("lse must be fp32 (B, heads, N)")
-    with torch.cuda.device(q.device):
-        check(lib.sana_window_anchor_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate),
-                                         _ptr(out), _ptr(lse), _stream()))
+    _call_on(q, lib.sana_window_anchor_fwd, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             _addr(gate), out.data_ptr(), _addr(lse))
     return out if lse is None else (out, lse)
 
 
@@ -738,10 +750,9 @@ def window_anchor_bwd(q, k, v, gate, out, lse, dy, heads, kv_heads, window, sink
     if ws is None:
         ws = _ws(lib.sana_window_anchor_bwd_workspace_size(ctypes.byref(s), int(gate is not None)), q.device)
     _same_device(q, ws)
-    with torch.cuda.device(q.device):
-        check(lib.sana_window_anchor_bwd(
-            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out), _ptr(lse), _ptr(dy),
-            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(ws), ws.numel(), _stream()))
+    _call_on(q, lib.sana_window_anchor_bwd, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             _addr(gate), out.data_ptr(), lse.data_ptr(), dy.data_ptr(), dq.data_ptr(),
+             dk.data_ptr(), dv.data_ptr(), _addr(dg), ws.data_ptr(), ws.numel())
     return dq, dk, dv, dg
 
 
@@ -777,11 +788,10 @@ def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_hea
     s = WindowDecodeShape(B, N, heads, kv_heads, D, k_cache.shape[1], window, sinks, scale)
     out = _out_like(out, "out", q, C)
     if ws is None:
-        ws = _ws(lib.sana_window_anchor_decode_workspace_size(ctypes.byref(s)), q.device)
-    with torch.cuda.device(q.device):
-        check(lib.sana_window_anchor_decode(
-            ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(k_cache), _ptr(v_cache),
-            _ptr(lengths), _ptr(out), _ptr(ws), ws.numel(), _stream()))
+        ws = _ws(lib.sana_window_anchor_decode_workspace_size(s), q.device)
+    _call_on(q, lib.sana_window_anchor_decode, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             _addr(gate), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
+             out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
