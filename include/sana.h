@@ -453,8 +453,8 @@ SANA_API sana_status sana_qk_norm_rope_bwd(const sana_qk_shape* shape, sana_dtyp
  *   negative length is an empty batch entry: nothing is appended, zeros come
  *   out.  capacity >= sinks + N.  Workspace:
  *   sana_window_anchor_decode_workspace_size() bytes, 256-byte aligned.
- * Errors: SANA_ERR_INVALID_ARG for NULL, misaligned (16 bytes) or aliasing
- * buffers and bad sizes or strides; SANA_ERR_UNSUPPORTED for a head_dim other
+ * Errors: SANA_ERR_INVALID_ARG for NULL, misaligned (16 bytes; lse and lengths
+ * 4) or aliasing buffers and bad sizes or strides; SANA_ERR_UNSUPPORTED for a head_dim other
  * than 128 and sizes past the limits.
  * ------------------------------------------------------------------------- */
 typedef struct {

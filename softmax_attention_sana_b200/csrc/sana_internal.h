@@ -29,7 +29,7 @@ unsigned long long current_context_id();
 // runs before its attributes are set.
 enum AttrKey : int {
   kAttrLinattn = 0, kAttrLinattnBwd, kAttrAnchor, kAttrGemm, kAttrMx128, kAttrMx256, kAttrWindowFwd,
-  kAttrWindowBwd, kAttrKeys
+  kAttrWindowBwd, kAttrWindowDecode, kAttrKeys
 };
 void once_per_context(int key, void (*set)());
 // Device address of the status word of the current device.

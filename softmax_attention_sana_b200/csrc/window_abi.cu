@@ -9,11 +9,10 @@ namespace {
 constexpr int kHeadDim = 128;
 constexpr int kMost = 1 << 30;  // positions, window, sinks, block: sums of two stay in 32 bits
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 struct Range {
   const void* p;
   size_t bytes;
+  unsigned align = 16;
 };
 bool overlap(const Range& a, const Range& b) {
   if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
@@ -21,9 +20,11 @@ bool overlap(const Range& a, const Range& b) {
   return x < y + b.bytes && y < x + a.bytes;
 }
 sana_status check_buffers(const char* who, const Range* in, int n_in, const Range* out, int n_out) {
-  for (int i = 0; i < n_in + n_out; ++i)
-    if (!aligned16(i < n_in ? in[i].p : out[i - n_in].p))
-      return fail(SANA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  for (int i = 0; i < n_in + n_out; ++i) {
+    const Range& r = i < n_in ? in[i] : out[i - n_in];
+    if (reinterpret_cast<uintptr_t>(r.p) % r.align)
+      return fail(SANA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned (lse: 4)", who);
+  }
   for (int o = 0; o < n_out; ++o) {
     for (int i = 0; i < n_in; ++i)
       if (overlap(out[o], in[i])) return fail(SANA_ERR_INVALID_ARG, "%s: an output aliases an input", who);
@@ -99,6 +100,9 @@ sana_status check_decode(const char* who, const sana_window_decode_shape* s, Dec
     return fail(SANA_ERR_UNSUPPORTED, "%s: capacity and window go up to 2^30, query rows of a key head to 65535", who);
   const long long tiles = ((long long)s->heads / s->kv_heads * s->N + 15) / 16;
   if (s->kv_heads * tiles > 65535) return fail(SANA_ERR_UNSUPPORTED, "%s: too many query rows", who);
+  // the tensor maps hold strides below 2^40 bytes
+  if ((unsigned long long)s->capacity * s->kv_heads * kHeadDim * 2 >= 1ULL << 40)
+    return fail(SANA_ERR_UNSUPPORTED, "%s: a cache may span 2^40 bytes at most", who);
   if (!std::isfinite(s->scale)) return fail(SANA_ERR_INVALID_ARG, "%s: scale must be finite", who);
   *c = DecodeCall{s->B, s->N, s->heads, s->kv_heads, s->capacity, s->window, s->sinks,
                   s->scale > 0.f ? s->scale : 1.f / sqrtf((float)kHeadDim)};
@@ -127,7 +131,7 @@ sana_status sana_window_anchor_fwd(const sana_window_shape* s, const void* q, co
   const long long tq = (long long)c.B * c.N, tk = (long long)c.B * c.N_keys;
   const Range in[] = {{q, span(tq, c.q_stride, c.heads)}, {k, span(tk, c.k_stride, c.kv_heads)},
                       {v, span(tk, c.v_stride, c.kv_heads)}, {g, span(tq, c.gate_stride, c.heads)}};
-  const Range outs[] = {{out, (size_t)tq * c.heads * kHeadDim * 2}, {lse, (size_t)tq * c.heads * 4}};
+  const Range outs[] = {{out, (size_t)tq * c.heads * kHeadDim * 2}, {lse, (size_t)tq * c.heads * 4, 4}};
   if (sana_status e = check_buffers(who, in, 4, outs, 2)) return e;
   if (overlap({c.lengths, (size_t)c.B * 4}, outs[0]) || overlap({c.lengths, (size_t)c.B * 4}, outs[1]))
     return fail(SANA_ERR_INVALID_ARG, "%s: an output aliases the lengths", who);
@@ -167,7 +171,7 @@ sana_status sana_window_anchor_bwd(const sana_window_shape* s, const void* q, co
   const size_t need = window_bwd_ws_bytes(c);
   const Range in[] = {{q, span(tq, c.q_stride, c.heads)}, {k, span(tk, c.k_stride, c.kv_heads)},
                       {v, span(tk, c.v_stride, c.kv_heads)}, {g, span(tq, c.gate_stride, c.heads)},
-                      {out, nq}, {lse, (size_t)tq * c.heads * 4}, {dy, nq}};
+                      {out, nq}, {lse, (size_t)tq * c.heads * 4, 4}, {dy, nq}};
   const Range outs[] = {{dq, nq}, {dk, nk}, {dv, nk}, {dg, nq}, {ws, need}};
   if (sana_status e = check_buffers(who, in, 7, outs, 5)) return e;
   for (const Range& o : outs)

@@ -85,61 +85,68 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 }
 
 // ---------------------------------------------------------------- prep
-// A half-warp per (batch, row, head); rows [N, N_pad) only get their statistics.
+// A CTA takes 32 consecutive rows of one head (so that their statistics, which
+// lie together, are written together; CTAs of neighbouring heads run side by side
+// and share DRAM pages), a half-warp two of them.  Rows [N, n_pad) only get their
+// statistics.
+constexpr int kPrepRows = 32;
 template <bool kGate>
 __global__ void __launch_bounds__(256)
     window_prep_kernel(const __nv_bfloat16* __restrict__ y, const __nv_bfloat16* __restrict__ dy,
                        const __nv_bfloat16* __restrict__ gate, long long gate_stride,
-                       const float* __restrict__ lse, const WindowDev w, int B, int n_pad,
+                       const float* __restrict__ lse, const WindowDev w, int n_pad,
                        float* __restrict__ nlse, float* __restrict__ ndelta,
                        __nv_bfloat16* __restrict__ d_o, __nv_bfloat16* __restrict__ dg) {
-  const int sub = threadIdx.x & 15;
-  const long long id = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const long long rows = (long long)B * n_pad * w.heads;
-  // whole half-warps past the end have nothing to do, but take part in the shuffles
-  const bool in = id < rows;
-  const int h = in ? (int)(id % w.heads) : 0;
-  const long long bn = in ? id / w.heads : 0;
-  const int b = (int)(bn / n_pad), n = (int)(bn % n_pad);
-  const bool real = in && n < w.N;
-  const bool live = real && w.off + n < window_length(w, b);
-  const size_t tok = (size_t)b * w.N + n;
-  const size_t at = (tok * w.heads + h) * kD + sub * 8;
-  float sum = 0.f;
-  uint32_t dow[4] = {0, 0, 0, 0}, dgw[4] = {0, 0, 0, 0};
-  if (live) {
-    const uint4 yv = __ldcs(reinterpret_cast<const uint4*>(y + at));
-    const uint4 dv = __ldcs(reinterpret_cast<const uint4*>(dy + at));
-    const uint32_t ya[4] = {yv.x, yv.y, yv.z, yv.w}, da[4] = {dv.x, dv.y, dv.z, dv.w};
-    uint32_t ga[4] = {0, 0, 0, 0};
-    if (kGate) {
-      const uint4 gv = __ldcs(reinterpret_cast<const uint4*>(gate + tok * gate_stride + (size_t)h * kD + sub * 8));
-      ga[0] = gv.x; ga[1] = gv.y; ga[2] = gv.z; ga[3] = gv.w;
-    }
+  const int sub = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  const int h = blockIdx.x % w.heads, b = blockIdx.z;
+  const int len = window_length(w, b);
+  const int n0 = blockIdx.x / w.heads * kPrepRows + hw;  // and n0 + 16
+  uint4 yv[2], dv[2], gv[2];
+  bool live[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = bf2_to_f2(ya[i]), d = bf2_to_f2(da[i]);
+  for (int i = 0; i < 2; ++i) {
+    const int n = n0 + 16 * i;
+    live[i] = n < w.N && w.off + n < len;
+    const size_t tok = (size_t)b * w.N + n, at = (tok * w.heads + h) * kD + sub * 8;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    yv[i] = live[i] ? __ldcs(reinterpret_cast<const uint4*>(y + at)) : zero;
+    dv[i] = live[i] ? __ldcs(reinterpret_cast<const uint4*>(dy + at)) : zero;
+    gv[i] = zero;
+    if (kGate && live[i])
+      gv[i] = __ldcs(reinterpret_cast<const uint4*>(gate + tok * gate_stride + (size_t)h * kD + sub * 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = n0 + 16 * i;
+    const uint32_t ya[4] = {yv[i].x, yv[i].y, yv[i].z, yv[i].w}, da[4] = {dv[i].x, dv[i].y, dv[i].z, dv[i].w};
+    const uint32_t ga[4] = {gv[i].x, gv[i].y, gv[i].z, gv[i].w};
+    uint32_t dow[4] = {0, 0, 0, 0}, dgw[4] = {0, 0, 0, 0};
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = bf2_to_f2(ya[k]), d = bf2_to_f2(da[k]);
       const float t0 = a.x * d.x, t1 = a.y * d.y;
       sum += t0 + t1;
       if (kGate) {
-        const float2 g = bf2_to_f2(ga[i]);
-        dow[i] = f2_to_bf2(d.x * sigmoid_fast(g.x), d.y * sigmoid_fast(g.y));
-        dgw[i] = f2_to_bf2(t0 * sigmoid_fast(-g.x), t1 * sigmoid_fast(-g.y));
+        const float2 g = bf2_to_f2(ga[k]);
+        dow[k] = f2_to_bf2(d.x * sigmoid_fast(g.x), d.y * sigmoid_fast(g.y));
+        dgw[k] = f2_to_bf2(t0 * sigmoid_fast(-g.x), t1 * sigmoid_fast(-g.y));
       }
     }
-  }
 #pragma unroll
-  for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-  if (kGate && real) {
-    *reinterpret_cast<uint4*>(d_o + at) = make_uint4(dow[0], dow[1], dow[2], dow[3]);
-    __stcs(reinterpret_cast<uint4*>(dg + at), make_uint4(dgw[0], dgw[1], dgw[2], dgw[3]));
-  }
-  if (in && sub == 0) {
-    const size_t row = (size_t)b * w.heads + h;
-    // a row that sees nothing has lse = -inf; its terms are 2^-inf here
-    const float l = live ? lse[row * w.N + n] : -INFINITY;
-    nlse[row * n_pad + n] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-    ndelta[row * n_pad + n] = live ? -sum : 0.f;
+    for (int k = 8; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (kGate && n < w.N) {  // (zeros for padding)
+      const size_t at = (((size_t)b * w.N + n) * w.heads + h) * kD + sub * 8;
+      *reinterpret_cast<uint4*>(d_o + at) = make_uint4(dow[0], dow[1], dow[2], dow[3]);
+      __stcs(reinterpret_cast<uint4*>(dg + at), make_uint4(dgw[0], dgw[1], dgw[2], dgw[3]));
+    }
+    if (n < n_pad && sub == 0) {
+      const size_t row = (size_t)b * w.heads + h;
+      // a row that sees nothing has lse = -inf; its terms are 2^-inf here
+      const float l = live[i] ? lse[row * w.N + n] : -INFINITY;
+      nlse[row * n_pad + n] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+      ndelta[row * n_pad + n] = live[i] ? -sum : 0.f;
+    }
   }
 }
 
@@ -524,33 +531,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Sums the shares of the split key tiles in order.  One CTA per (split key tile
-// and one of dV, dK; key head; batch); thread = 4 columns of a row per pass.
-__global__ void __launch_bounds__(512)
+// Sums the shares of the split key tiles in order.  One CTA per (slice of 16 rows
+// of a split key tile's dV or dK; key head; batch); thread = 4 columns of a row.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(kJoinRows * kD / 4)
     window_join_kernel(const float* __restrict__ part, const WindowDev w, const DkvPlan plan,
                        int items, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
-  const int hk = blockIdx.y, b = blockIdx.z, which = blockIdx.x & 1;
+  constexpr int kSlices = kRows / kJoinRows;
+  const int hk = blockIdx.y, b = blockIdx.z, slice = blockIdx.x % kSlices;
+  const int which = blockIdx.x / kSlices & 1, s = blockIdx.x / (2 * kSlices);
   const int split_sinks = plan.sink_parts > 1 ? plan.sink_tiles : 0;
-  const int s = blockIdx.x >> 1;
   const int kt = s < split_sinks ? s : plan.sink_tiles + (s - split_sinks);
   const bool sink = kt < plan.sink_tiles;
   const int item = sink ? kt * plan.sink_parts
                         : plan.sink_tiles * plan.sink_parts + (kt - plan.sink_tiles) * plan.win_parts;
   const QSpan qs = query_span(w, kt, window_length(w, b));
   const int n = (w.heads / w.kv_heads * qs.count + plan.chunk - 1) / plan.chunk;  // shares written
-  const float* p = part + ((((size_t)b * w.kv_heads + hk) * items + item) * 2 + which) * kRows * kD;
-  __nv_bfloat16* dst = which ? dk : dv;
-  for (int i = threadIdx.x; i < kRows * kD / 4; i += 512) {
-    const int j = kt * kRows + i / (kD / 4);
-    if (j >= w.N_keys) break;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < n; ++k) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (size_t)k * 2 * kRows * kD) + i);
-      a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
-    }
-    *reinterpret_cast<uint2*>(dst + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + (i % (kD / 4)) * 4) =
-        make_uint2(f2_to_bf2(a.x, a.y), f2_to_bf2(a.z, a.w));
+  const int i = slice * kJoinRows * (kD / 4) + threadIdx.x, j = kt * kRows + i / (kD / 4);
+  if (j >= w.N_keys) return;
+  const float4* p = reinterpret_cast<const float4*>(
+                        part + ((((size_t)b * w.kv_heads + hk) * items + item) * 2 + which) * kRows * kD) + i;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
+    const float4 v = __ldcs(p + (size_t)k * 2 * kRows * kD / 4);
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
+  *reinterpret_cast<uint2*>((which ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + (i % (kD / 4)) * 4) =
+      make_uint2(f2_to_bf2(a.x, a.y), f2_to_bf2(a.z, a.w));
 }
 
 // ---------------------------------------------------------------- dq
@@ -896,14 +904,13 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
     cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDqSmem + sizeof(DqCtl)));
   });
   using bf = __nv_bfloat16;
-  const long long rows = (long long)c.B * n_pad * c.heads;
-  const unsigned prep = (unsigned)((rows + 15) / 16);
+  const dim3 prep((unsigned)c.heads * (unsigned)(n_pad / kPrepRows), 1, c.B);
   if (c.gate)
     window_prep_kernel<true><<<prep, 256, 0, st>>>((const bf*)y, (const bf*)dy, (const bf*)c.gate, c.gate_stride, lse,
-                                                   w, c.B, n_pad, m.nlse, m.ndelta, m.d_o, (bf*)dg);
+                                                   w, n_pad, m.nlse, m.ndelta, m.d_o, (bf*)dg);
   else
-    window_prep_kernel<false><<<prep, 256, 0, st>>>((const bf*)y, (const bf*)dy, nullptr, 0, lse, w, c.B, n_pad,
-                                                    m.nlse, m.ndelta, nullptr, nullptr);
+    window_prep_kernel<false><<<prep, 256, 0, st>>>((const bf*)y, (const bf*)dy, nullptr, 0, lse, w, n_pad, m.nlse,
+                                                    m.ndelta, nullptr, nullptr);
   if (sana_status e = check_launch("window_prep_kernel")) return e;
   const float sl = c.scale * kLog2e;
   int* sw = status_word();
@@ -914,7 +921,7 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
   if (sana_status e = check_launch("window_dkv_kernel")) return e;
   const int split = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.win_parts > 1 ? p.tiles - p.sink_tiles : 0);
   if (split) {
-    window_join_kernel<<<dim3(2 * split, c.kv_heads, c.B), 512, 0, st>>>(m.part, w, p, items, (bf*)dk, (bf*)dv);
+    window_join_kernel<<<dim3(2 * split * (kRows / kJoinRows), c.kv_heads, c.B), kJoinRows * kD / 4, 0, st>>>(m.part, w, p, items, (bf*)dk, (bf*)dv);
     if (sana_status e = check_launch("window_join_kernel")) return e;
   }
   window_dq_kernel<<<dim3((c.N + kRows - 1) / kRows, c.heads, c.B), kThreads, kDqSmem + sizeof(DqCtl), st>>>(

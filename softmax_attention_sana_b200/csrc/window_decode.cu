@@ -4,24 +4,21 @@
 // Bound by HBM: every visible key and value row is read once (512 bytes for
 // 4 * 128 flops per query row), so the work is split over the keys until all
 // SMs load, and the arithmetic only has to keep up.  That is what the warp-wide
-// m16n8k16 products do here, straight from registers: a tcgen05 tile would put
-// 128 keys against 8 query rows through shared memory and TMEM, a longer way
-// for the same bytes.
+// m16n8k16 products do here: a tcgen05 tile would put 128 keys against 8 query
+// rows through TMEM, a longer way for the same bytes.
 //
-// The query rows of one key head (N tokens x heads / kv_heads) form tiles of 8
-// (NT of them, 1 or 2, per CTA).  A warp takes 16 keys at a time:
-//   S^T (16 keys x 8 rows) = K Q^T   A = K: lane (a = lane / 4, c = lane % 4)
-//       holds 16-byte pieces c, c + 4, c + 8, c + 12 of keys a and a + 8; the
-//       order of d inside a product is free as long as Q uses the same one, so
-//       the pieces feed the products as loaded
+// The visible keys of a sequence are a few runs of slots (sinks, the window up
+// to the ring's end and from its start, the new tokens), cut into tiles of 64.  A
+// CTA takes a share of the tiles of one key head: a producer warp brings them in
+// by TMA (boxes of 16 rows, only those that hold visible keys) through a ring of
+// three stages, four warps take 16 keys of each.  The query rows of the key head
+// (N tokens x heads / kv_heads) form tiles of 8 (NT of them, 1 or 2, per CTA):
+//   S^T (16 keys x 8 rows) = K Q^T      A = K by ldmatrix
 //   P^T = 2^(sl S^T - m) in bf16, turned to (row, key) order by movmatrix
-//   O^T (128 d x 8 rows) += V^T P^T   A = V^T: the lane holds 16-byte pieces a
-//       and a + 8 of keys 2c, 2c + 1, 2c + 8, 2c + 9; a byte permutation pairs
-//       two keys per d, and product e of 8 covers d = 8a + e and 64 + 8a + e
-// K of the next 16 keys is requested as soon as the scores are made, V as soon
-// as it is used: 8 KB stay in flight per warp with no shared memory.  Running
-// maximum and sum in fp32; the warps of a CTA and then the CTAs of a (sequence,
-// key head) are joined in a fixed order.
+//   O^T (128 d x 8 rows) += V^T P^T     A = V^T by ldmatrix.trans
+// Running maximum and sum in fp32; the warps of a CTA and then the CTAs of a
+// (sequence, key head) are joined in a fixed order.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
@@ -32,8 +29,13 @@ namespace sana {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kWarps = 4;
-constexpr int kKeys = 16;  // keys a warp takes at a time
+constexpr int kWarps = 4;               // consumer warps; one more warp loads
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = 64;               // keys of a tile: 16 for each warp
+constexpr int kBox = 16;                // rows of a TMA box
+constexpr int kStages = 3;
+constexpr int kHalf = kTile * 128;      // 64 columns of a tile's K or V, 8 KB
+constexpr int kStageB = 4 * kHalf;      // K and V of a tile, 32 KB
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeDev {
@@ -46,52 +48,76 @@ struct DecodeDev {
   float* part;    // [item][split][8 NT rows][128] sums, then [..][2] max and sum
 };
 
-// The keys of one sequence in this call: m in [0, S) sinks at position m, then
-// positions lo, lo + 1, ... up to the new tokens at [len, len + N).
-struct KeyList {
-  int S, count;
-  long long lo, len;  // positions may pass 2^31 by the N new tokens
-  long long slot_lo;  // slot of position lo
-  __device__ __forceinline__ long long pos(int m) const { return m < S ? m : lo + (m - S); }
+// The visible keys of one sequence: runs of slots (runs 0..2; run 3: rows of the
+// new tokens) that hold consecutive positions.
+struct KeyRuns {
+  long long pos[4];  // positions may pass 2^31 by the N new tokens
+  int slot[4], rows[4], tiles;
+  // Tile t: its run, and its first row there.
+  __device__ __forceinline__ void tile(int t, int& run, int& row) const {
+    run = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int n = (rows[i] + kTile - 1) / kTile;
+      if (run == i && t >= n) {
+        t -= n;
+        run = i + 1;
+      }
+    }
+    row = t * kTile;
+  }
 };
-__device__ __forceinline__ KeyList key_list(const DecodeDev& d, int len) {
-  KeyList k;
+__device__ __forceinline__ KeyRuns key_runs(const DecodeDev& d, int len) {
+  KeyRuns k;
   const long long ring = d.capacity - d.sinks, total = (long long)len + d.N;
-  k.len = len;
-  k.lo = 0;
-  if (d.window && len + 1LL - d.window > k.lo) k.lo = len + 1LL - d.window;
-  if (total - ring > k.lo && total > d.capacity) k.lo = total - ring;
-  k.S = (int)(k.lo < d.sinks ? k.lo : d.sinks);
-  k.count = (int)(k.S + total - k.lo);
-  k.slot_lo = k.lo < d.capacity ? k.lo : d.sinks + (k.lo - d.sinks) % ring;
+  // first position of the window of the first new token that the ring still
+  // holds once all N are in
+  long long lo = 0;
+  if (d.window && len + 1LL - d.window > lo) lo = len + 1LL - d.window;
+  if (total > d.capacity && total - ring > lo) lo = total - ring;
+  const int old = (int)(len - lo);  // keys of the window in the cache
+  const int s = (int)(lo < d.sinks ? lo : d.sinks);
+  const int at = (int)(lo < d.capacity ? lo : d.sinks + (lo - d.sinks) % ring);
+  const int upto = min(old, d.capacity - at);
+  k.pos[0] = 0;
+  k.slot[0] = 0;
+  k.rows[0] = s;
+  k.pos[1] = lo;
+  k.slot[1] = at;
+  k.rows[1] = upto;
+  if (at == s) {  // the window follows the sinks: one run
+    k.rows[0] += upto;
+    k.rows[1] = 0;
+  }
+  k.pos[2] = lo + upto;
+  k.slot[2] = d.sinks;
+  k.rows[2] = old - upto;
+  k.pos[3] = len;
+  k.slot[3] = 0;
+  k.rows[3] = d.N;
+  k.tiles = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k.tiles += (k.rows[i] + kTile - 1) / kTile;
   return k;
 }
-// Row of key m: in the new tokens, or in its slot (at most one turn of the ring
-// after lo's).
-__device__ __forceinline__ const __nv_bfloat16* key_row(const DecodeDev& d, const KeyList& k,
-                                                        const __nv_bfloat16* cache,
-                                                        const __nv_bfloat16* fresh, int m) {
-  const long long p = k.pos(m);
-  const size_t pitch = (size_t)d.kv_heads * kD;
-  if (p >= k.len) return fresh + (size_t)(p - k.len) * pitch;
-  long long s = m < k.S ? m : k.slot_lo + (m - k.S);
-  if (s >= d.capacity) s -= d.capacity - d.sinks;
-  return cache + (size_t)s * pitch;
-}
 
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
       " {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // 8 x 8 transpose of 16-bit values across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -111,11 +137,23 @@ __device__ __forceinline__ void write_out(const DecodeDev& d, int b, int hk, int
   d.out[at] = __float2bfloat16(y);
 }
 
+struct DecodeCtl {
+  uint64_t full[kStages], empty[kStages];
+  int abort_flag;
+};
+// Dynamic shared memory: the ring; when its last tile is used, the warps' sums.
+constexpr size_t kDecodeSmem = kStages * (size_t)kStageB + 1024;
+
 template <int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) window_decode_kernel(const DecodeDev d) {
+__global__ void __launch_bounds__(kThreads, 2)
+    window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+                         const DecodeDev d, int* status) {
   constexpr int kRowsT = 8 * NT;
-  __shared__ float sm_o[kWarps][kRowsT][kD + 4];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ DecodeCtl ctl;
   __shared__ float sm_m[kWarps][kRowsT], sm_l[kWarps][kRowsT];
+  uint8_t* ring = align1024(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, a = lane >> 2, c = lane & 3;
   const int splits = gridDim.x, split = blockIdx.x, b = blockIdx.z;
   const int hk = blockIdx.y / d.row_tiles, rt = blockIdx.y - hk * d.row_tiles;
@@ -125,153 +163,180 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) window_decode_ke
 
   if (len < 0) {  // an empty batch entry
     if (split == 0)
-      for (int i = threadIdx.x; i < min(kRowsT, rows - row0) * kD; i += 32 * kWarps)
+      for (int i = threadIdx.x; i < min(kRowsT, rows - row0) * kD; i += kThreads)
         write_out(d, b, hk, row0 + i / kD, i % kD, 0.f, 0.f);
     return;
   }
-  const KeyList keys = key_list(d, len);
-  const size_t pitch = (size_t)d.kv_heads * kD;
-  const __nv_bfloat16* kn = d.k_new + ((size_t)b * d.N * d.kv_heads + hk) * kD;
-  const __nv_bfloat16* vn = d.v_new + ((size_t)b * d.N * d.kv_heads + hk) * kD;
-  __nv_bfloat16* kc = d.k_cache + ((size_t)b * d.capacity * d.kv_heads + hk) * kD;
-  __nv_bfloat16* vc = d.v_cache + ((size_t)b * d.capacity * d.kv_heads + hk) * kD;
-
-  // The new tokens go to their slots.  What a slot held before is a position
-  // that no query of this call sees, so nobody reads it meanwhile.
-  if (split == 0 && rt == 0) {
-    for (int i = threadIdx.x; i < d.N * 32; i += 32 * kWarps) {
-      const int t = i >> 5, piece = (i & 15) * 8;
-      const long long p = keys.len + t;
-      const size_t s = p < d.capacity ? (size_t)p : (size_t)(d.sinks + (p - d.sinks) % (d.capacity - d.sinks));
-      const bool is_v = (i & 16) != 0;
-      *reinterpret_cast<uint4*>((is_v ? vc : kc) + s * pitch + piece) =
-          *reinterpret_cast<const uint4*>((is_v ? vn : kn) + (size_t)t * pitch + piece);
+  const KeyRuns keys = key_runs(d, len);
+  const int per = (keys.tiles + splits - 1) / splits;
+  const int t0 = min(split * per, keys.tiles), count = min(per, keys.tiles - t0);
+  const WaitCtx wc{&ctl.abort_flag, status};
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl.full[i], 1);
+      mbar_init(&ctl.empty[i], kWarps);
     }
+    ctl.abort_flag = 0;
+    mbar_fence_init();
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ------------------------------------------------ producer
+    if (lane == 0) {
+      int n = 0;
+      for (int t = 0; t < count; ++t) {
+        const int st = t % kStages;
+        if (t >= kStages && !mbar_wait(&ctl.empty[st], ((t / kStages) - 1) & 1, wc, 0xc1)) break;
+        int run, row;
+        keys.tile(t0 + t, run, row);
+        const int boxes = (min(kTile, keys.rows[run] - row) + kBox - 1) / kBox;
+        const CUtensorMap* mk = run == 3 ? &tm_kn : &tm_k;
+        const CUtensorMap* mv = run == 3 ? &tm_vn : &tm_v;
+        uint8_t* dst = ring + st * kStageB;
+        mbar_arrive_expect_tx(&ctl.full[st], boxes * 4 * kBox * 128);
+        for (int x = 0; x < boxes; ++x)  // (rows past the cache's end read as zeros)
+          for (int hh = 0; hh < 2; ++hh) {
+            tma_load_3d(dst + hh * kHalf + x * kBox * 128, mk, &ctl.full[st], hk * kD + hh * 64, keys.slot[run] + row + x * kBox, b);
+            tma_load_3d(dst + (2 + hh) * kHalf + x * kBox * 128, mv, &ctl.full[st], hk * kD + hh * 64, keys.slot[run] + row + x * kBox, b);
+          }
+        ++n;
+      }
+      if (*wc.abort_flag)  // loads still in flight land before the CTA exits
+        for (int t = n > kStages ? n - kStages : 0; t < n; ++t) mbar_drain(&ctl.full[t % kStages], (t / kStages) & 1);
+    }
+    // The new tokens go to their slots.  What a slot held before is a position
+    // that no query of this call sees; a box may touch it, its rows are masked.
+    if (split == 0 && rt == 0) {
+      const size_t pitch = (size_t)d.kv_heads * kD, new0 = ((size_t)b * d.N * d.kv_heads + hk) * kD;
+      const size_t cache0 = ((size_t)b * d.capacity * d.kv_heads + hk) * kD;
+      for (int t = 0; t < d.N; ++t) {
+        const long long p = (long long)len + t;
+        const size_t s = p < d.capacity ? (size_t)p : (size_t)(d.sinks + (p - d.sinks) % (d.capacity - d.sinks));
+        const size_t piece = (lane & 15) * 8;
+        const __nv_bfloat16* src = (lane & 16 ? d.v_new : d.k_new) + new0 + t * pitch + piece;
+        *reinterpret_cast<uint4*>((lane & 16 ? d.v_cache : d.k_cache) + cache0 + s * pitch + piece) =
+            *reinterpret_cast<const uint4*>(src);
+      }
+    }
+    __syncthreads();  // the ring has become the warps' sums
+    __syncthreads();
+    return;
   }
 
-  // this CTA's groups of 16 keys, and this warp's: g, g + 4, ...
-  const int groups = (keys.count + kKeys - 1) / kKeys;
-  const int per = (groups + splits - 1) / splits;
-  const int g1 = min(groups, (split + 1) * per);
-  int g = split * per + warp;
-
-  uint4 kr[2][4], vr[4][2];
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  auto load_k = [&](int gg) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = gg * kKeys + a + 8 * i;
-      const bool in = gg < g1 && m < keys.count;
-      const __nv_bfloat16* p = in ? key_row(d, keys, kc, kn, m) : nullptr;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kr[i][j] = in ? load16(p + (c + 4 * j) * 8) : zero;
-    }
-  };
-  auto load_v = [&](int gg) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = gg * kKeys + 2 * c + (i & 1) + 8 * (i >> 1);
-      const bool in = gg < g1 && m < keys.count;
-      const __nv_bfloat16* p = in ? key_row(d, keys, vc, vn, m) : nullptr;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) vr[i][j] = in ? load16(p + a * 8 + 64 * j) : zero;
-    }
-  };
-  load_k(g);
-  load_v(g);
-
-  // Q: row a of each tile, the same pieces of d as K's
-  uint4 qr[NT][4];
+  // ------------------------------------------------ consumers
+  // Q as B operand: row a of each tile, d = 16 j + 2 c (+ 8)
+  uint32_t qr[NT][8][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int row = row0 + t * 8 + a;
-    const __nv_bfloat16* p = d.q + (((size_t)b * d.N + row / group) * d.heads + hk * group + row % group) * kD;
+    const __nv_bfloat16* p = d.q + (((size_t)b * d.N + row / group) * d.heads + hk * group + row % group) * kD + 2 * c;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) qr[t][j] = row < rows ? *reinterpret_cast<const uint4*>(p + (c + 4 * j) * 8) : zero;
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qr[t][j][e] = row < rows ? *reinterpret_cast<const uint32_t*>(p + 16 * j + 8 * e) : 0u;
   }
-  // position of query rows 2c, 2c + 1 of each tile
-  long long qpos[NT][2];
+  long long qpos[NT][2];  // position of query rows 2c, 2c + 1 of each tile
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) qpos[t][e] = keys.len + min(row0 + t * 8 + 2 * c + e, rows - 1) / group;
+    for (int e = 0; e < 2; ++e) qpos[t][e] = (long long)len + min(row0 + t * 8 + 2 * c + e, rows - 1) / group;
   const bool one = d.N == 1;  // then every listed key is visible
 
-  float o[NT][8][4] = {};
+  float o[NT][8][4] = {};  // [d / 16][2 (d / 8 % 2) + row % 2]: d = 16 j + a (+ 8), rows 2c, 2c + 1
   float mx[NT][2], sum[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) mx[t][e] = -INFINITY, sum[t][e] = 0.f;
-
-  for (; g < g1; g += kWarps) {
-    float s[NT][4] = {};
+  // ldmatrix rows of this lane: K: key lane % 16, piece lane / 16; V: key lane % 8 +
+  // 8 (lane / 16), piece lane / 8 % 2
+  const int k_row = warp * 16 + (lane & 15), k_piece = lane >> 4;
+  const int v_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3), v_piece = (lane >> 3) & 1;
+  bool ok = true;
+  for (int u = 0; u < count; ++u) {
+    const int st = u % kStages;
+    int run, row;
+    keys.tile(t0 + u, run, row);
+    ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[st], (u / kStages) & 1, wc, 0xc2));
+    if (!ok) break;
+    const int left = keys.rows[run] - row - warp * 16;  // keys of this warp
+    if (left > 0) {
+      const uint32_t kb = smem_u32(ring + st * kStageB), vb = kb + 2 * kHalf;
+      float s[NT][4] = {};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j) {
+        uint32_t ka[4];
+        ldsm4(ka, kb + (j >> 2) * kHalf + sw128_off(k_row, (j & 3) * 2 + k_piece));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816(s[t], ka, qr[t][j][0], qr[t][j][1]);
+      }
+      // s[t][e + 2 i]: key a + 8 i, query row 2c + e
+      uint32_t p0[NT], p1[NT];
+      const long long first = keys.pos[run] + row + warp * 16;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        mma16816(s[t], kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y, qr[t][j].x, qr[t][j].y);
-        mma16816(s[t], kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w, qr[t][j].z, qr[t][j].w);
-      }
-    load_k(g + kWarps);
-    // s[t][e + 2 i]: key a + 8 i, query row 2c + e
-    uint32_t p0[NT], p1[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+        for (int i = 0; i < 2; ++i) {
+          const bool in = a + 8 * i < left;
+          const long long p = first + a + 8 * i;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int m = g * kKeys + a + 8 * i;
-        const bool in = m < keys.count;
-        const long long p = keys.pos(m);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool sees = in && (one || (p <= qpos[t][e] &&
-                                           (d.window == 0 || p > qpos[t][e] - d.window || p < d.sinks)));
-          s[t][e + 2 * i] = sees ? s[t][e + 2 * i] * d.sl : -INFINITY;
-        }
-      }
-      float f[2][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = fmaxf(s[t][e], s[t][e + 2]);
-#pragma unroll
-        for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        const float now = fmaxf(mx[t][e], top);
-        const float ref = now == -INFINITY ? 0.f : now;
-        const float corr = ex2(mx[t][e] - ref);  // 1 where the maximum stayed, 0 before the first key
-        if (__any_sync(0xffffffffu, now != mx[t][e])) {
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            o[t][n][e] *= corr;
-            o[t][n][e + 2] *= corr;
+          for (int e = 0; e < 2; ++e) {
+            const bool sees = in && (one || (p <= qpos[t][e] &&
+                                             (d.window == 0 || p > qpos[t][e] - d.window || p < d.sinks)));
+            s[t][e + 2 * i] = sees ? s[t][e + 2 * i] * d.sl : -INFINITY;
           }
         }
-        mx[t][e] = now;
-        f[e][0] = ex2(s[t][e] - ref);
-        f[e][1] = ex2(s[t][e + 2] - ref);
-        sum[t][e] = sum[t][e] * corr + (f[e][0] + f[e][1]);
+        float f[2][2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = fmaxf(s[t][e], s[t][e + 2]);
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+          const float now = fmaxf(mx[t][e], top);
+          const float ref = now == -INFINITY ? 0.f : now;
+          const float corr = ex2(mx[t][e] - ref);  // 1 where the maximum stayed, 0 before the first key
+          if (__any_sync(0xffffffffu, now != mx[t][e])) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              o[t][n][e] *= corr;
+              o[t][n][e + 2] *= corr;
+            }
+          }
+          mx[t][e] = now;
+          f[e][0] = ex2(s[t][e] - ref);
+          f[e][1] = ex2(s[t][e + 2] - ref);
+          sum[t][e] = sum[t][e] * corr + (f[e][0] + f[e][1]);
+        }
+        p0[t] = transpose8(f2_to_bf2(f[0][0], f[1][0]));
+        p1[t] = transpose8(f2_to_bf2(f[0][1], f[1][1]));
       }
-      p0[t] = transpose8(f2_to_bf2(f[0][0], f[1][0]));
-      p1[t] = transpose8(f2_to_bf2(f[0][1], f[1][1]));
-    }
+      // rows of V past the run hold anything (P is 0 there): keys 2c, 2c + 1 and + 8
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (left < 16) {
+        keep0 = (2 * c < left ? 0xffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
+        keep1 = (2 * c + 8 < left ? 0xffffu : 0u) | (2 * c + 9 < left ? 0xffff0000u : 0u);
+      }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      auto word = [&](const uint4& v) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; };
+      for (int j = 0; j < 8; ++j) {
+        uint32_t va[4];
+        ldsm4_trans(va, vb + (j >> 2) * kHalf + sw128_off(v_row, (j & 3) * 2 + v_piece));
+        va[0] &= keep0;
+        va[1] &= keep0;
+        va[2] &= keep1;
+        va[3] &= keep1;
 #pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const uint32_t sel = hi ? 0x7632 : 0x5410;
-        const uint32_t a0 = __byte_perm(word(vr[0][0]), word(vr[1][0]), sel);
-        const uint32_t a1 = __byte_perm(word(vr[0][1]), word(vr[1][1]), sel);
-        const uint32_t a2 = __byte_perm(word(vr[2][0]), word(vr[3][0]), sel);
-        const uint32_t a3 = __byte_perm(word(vr[2][1]), word(vr[3][1]), sel);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(o[t][2 * w + hi], a0, a1, a2, a3, p0[t], p1[t]);
+        for (int t = 0; t < NT; ++t) mma16816(o[t][j], va, p0[t], p1[t]);
       }
     }
-    load_v(g + kWarps);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.empty[st]);
   }
 
-  // join the warps: rows 2c + e, d = 8a + n and 64 + 8a + n
+  // join the warps: rows 2c + e, d = 16 j + a (+ 8)
+  __syncthreads();
+  float(*sm_o)[kRowsT][kD + 4] = reinterpret_cast<float(*)[kRowsT][kD + 4]>(ring);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -281,10 +346,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 3 : 2) window_decode_ke
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float* dst = &sm_o[warp][r][64 * hh + 8 * a];
-        *reinterpret_cast<float4*>(dst) = make_float4(o[t][0][e + 2 * hh], o[t][1][e + 2 * hh], o[t][2][e + 2 * hh], o[t][3][e + 2 * hh]);
-        *reinterpret_cast<float4*>(dst + 4) = make_float4(o[t][4][e + 2 * hh], o[t][5][e + 2 * hh], o[t][6][e + 2 * hh], o[t][7][e + 2 * hh]);
+      for (int j = 0; j < 8; ++j) {
+        sm_o[warp][r][16 * j + a] = o[t][j][e];
+        sm_o[warp][r][16 * j + a + 8] = o[t][j][e + 2];
       }
       if (a == 0) {
         sm_m[warp][r] = mx[t][e];
@@ -345,20 +409,30 @@ struct DecodePlan {
   int nt, row_tiles, splits;
 };
 // Rows: one tile of 8 where they fit, else tiles of 16 (a second pass over the
-// keys costs more than the registers of 16 rows).  Splits: three CTAs for every
-// SM, each with 64 keys (16 a warp) at least.
+// keys costs more than the registers of 16 rows).  Splits: of those that the key
+// tiles allow, the one whose waves of CTAs (two fit on an SM) are soonest done,
+// with a CTA's start and end counted as two tiles.  64 sequences, 2 key heads,
+// 8320 keys: 2 splits in one wave 93 us, 4 in two 97 us, 9 in four 106 us; 16
+// sequences, 24 key heads, 2052 keys: 1 split in two waves 89 us, 3 in four 80 us.
 DecodePlan decode_plan(const DecodeCall& c) {
   DecodePlan p{};
   const int rows = c.heads / c.kv_heads * c.N;
   p.nt = rows <= 8 ? 1 : 2;
   p.row_tiles = (rows + 8 * p.nt - 1) / (8 * p.nt);
-  const long long items = (long long)c.B * c.kv_heads * p.row_tiles;
+  const long long items = (long long)c.B * c.kv_heads * p.row_tiles, slots = 2 * kNumSMs;
   long long keys = c.capacity;
   if (c.window && (long long)c.window + c.sinks + c.N < keys) keys = (long long)c.window + c.sinks + c.N;
-  long long s = 3LL * kNumSMs / items;
-  const long long most = (keys + kWarps * kKeys - 1) / (kWarps * kKeys);
-  if (s > most) s = most;
-  p.splits = (int)(s < 1 ? 1 : s);
+  const long long tiles = (keys + kTile - 1) / kTile;
+  long long most = 4 * slots / items;  // four waves at most
+  most = most < 1 ? 1 : most > tiles ? tiles : most;
+  long long best = 0;
+  for (long long s = 1; s <= most; ++s) {
+    const long long cost = (items * s + slots - 1) / slots * ((tiles + s - 1) / s + 2);
+    if (best == 0 || cost < best) {
+      best = cost;
+      p.splits = (int)s;
+    }
+  }
   return p;
 }
 
@@ -378,9 +452,21 @@ sana_status window_decode_run(const DecodeCall& c, const void* q, const void* k_
   const DecodeDev d{(const bf*)q, (const bf*)k_new, (const bf*)v_new, (const bf*)gate, (bf*)k_cache, (bf*)v_cache,
                     (bf*)out, lengths, c.B, c.N, c.heads, c.kv_heads, c.capacity, c.window, c.sinks,
                     c.scale * kLog2e, p.row_tiles, (float*)ws};
+  const uint64_t C = (uint64_t)c.kv_heads * kD, cap = c.capacity, N = c.N;
+  CUtensorMap tk, tv, tkn, tvn;
+  if (!make_tmap_bf16_3d(&tk, k_cache, C, cap, c.B, C, cap * C, kBox) ||
+      !make_tmap_bf16_3d(&tv, v_cache, C, cap, c.B, C, cap * C, kBox) ||
+      !make_tmap_bf16_3d(&tkn, k_new, C, N, c.B, C, N * C, kBox) ||
+      !make_tmap_bf16_3d(&tvn, v_new, C, N, c.B, C, N * C, kBox))
+    return fail(SANA_ERR_CUDA, "windowed anchor step: cuTensorMapEncodeTiled failed");
+  once_per_context(kAttrWindowDecode, [] {
+    cudaFuncSetAttribute(window_decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+    cudaFuncSetAttribute(window_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+  });
+  int* sw = status_word();
   const dim3 grid(p.splits, c.kv_heads * p.row_tiles, c.B);
-  if (p.nt == 1) window_decode_kernel<1><<<grid, 32 * kWarps, 0, st>>>(d);
-  else window_decode_kernel<2><<<grid, 32 * kWarps, 0, st>>>(d);
+  if (p.nt == 1) window_decode_kernel<1><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
+  else window_decode_kernel<2><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
   if (sana_status e = check_launch("window_decode_kernel")) return e;
   if (p.splits > 1) {
     launch_dependent(window_decode_join_kernel, dim3(c.heads / c.kv_heads * c.N, c.kv_heads, c.B), dim3(kD), 0, st,

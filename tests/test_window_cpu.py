@@ -65,7 +65,7 @@ def test_workspace_sizes():
     assert size(1, 1000, 1000, 64, 64, 128, sinks=4) > plain   # the sinks' tile is split
     assert size(1, 1000, 1000, 2, 2, 0) > size(1, 1000, 1000, 2, 2, 0, head_dim=64) == 0
     dec = _lib.window_anchor_decode_workspace_size
-    assert dec(1, 1, 8, 8, 4096, 0) == 8 * 55 * 8 * 130 * 4
+    assert dec(1, 1, 8, 8, 4096, 0) == 8 * 32 * 8 * 130 * 4
     assert dec(512, 1, 8, 8, 4096, 0) == 0
 
 
