@@ -582,23 +582,28 @@ def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
     D = C // heads
     if (k is None) != (kv_heads == 0):
         raise ValueError("k is None exactly where kv_heads is 0")
-    if k is not None and (k.dtype != q.dtype or k.shape[:2] != q.shape[:2]):
-        raise ValueError("q and k must have one dtype and the same (B, N)")
-    s = QkShape(B, N, heads, kv_heads, D, _token_stride(q, "q", C),
-                0 if k is None else _token_stride(k, "k", kv_heads * D))
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (B, N) or
-                                  not positions.is_contiguous()):
-        raise ValueError("positions must be a contiguous int32 tensor (B, N)")
-    if isinstance(rotary, Rope):
-        if grid is None:
-            raise ValueError("a Rope needs the tokens' grid=(T, H, W)")
-        at = QkPositions(None, ctypes.pointer(rotary.struct), *grid, _addr(positions), offset)
-        table = rotary.tables
-    else:
+    k_stride = 0
+    if k is not None:
+        k_stride = _token_stride(k, "k", kv_heads * D)
+        Bk, Nk, _ = k.shape
+        if k.dtype is not q.dtype or Bk != B or Nk != N:
+            raise ValueError("q and k must have one dtype and the same (B, N)")
+    s = QkShape(B, N, heads, kv_heads, D, _token_stride(q, "q", C), k_stride)
+    at_positions = None
+    if positions is not None:
+        if positions.dtype is not torch.int32 or positions.shape != (B, N) or \
+                not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int32 tensor (B, N)")
+        at_positions = positions.data_ptr()
+    if isinstance(rotary, Rotary):
         if grid is not None:
             raise ValueError("grid goes with a Rope")
-        at = QkPositions(rotary.pointer, None, 0, 0, 0, _addr(positions), offset)
-        table = rotary.table
+        at, table = QkPositions(rotary.pointer, None, 0, 0, 0, at_positions, offset), rotary.table
+    else:
+        if grid is None:
+            raise ValueError("a Rope needs the tokens' grid=(T, H, W)")
+        at = QkPositions(None, ctypes.pointer(rotary.struct), *grid, at_positions, offset)
+        table = rotary.tables
     _same_device(q, k, positions, table)
     return s, at
 
@@ -613,11 +618,15 @@ def _norm_weight(w, name, q, D):
 
 
 def _out_like(out, name, q, width):
+    """A contiguous (B, N, width) tensor like q: `out`, checked, or a new one."""
+    B, N, C = q.shape
     if out is None:
-        return q.new_empty((*q.shape[:2], width))
+        if C == width and q.is_contiguous():
+            return torch.empty_like(q)
+        return q.new_empty((B, N, width))
     _need(out, name)
-    if out.dtype != q.dtype or tuple(out.shape) != (*q.shape[:2], width):
-        raise ValueError(f"{name} must be {q.dtype} {(*q.shape[:2], width)}")
+    if out.dtype is not q.dtype or out.shape != (B, N, width):
+        raise ValueError(f"{name} must be {q.dtype} {(B, N, width)}")
     _same_device(q, out)
     return out
 
@@ -683,26 +692,29 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv
 
 def _window_shape(q, k, v, gate, heads, kv_heads, window, sinks, block, lengths, scale):
     """The shape struct of a call on q, gate (B, N, heads * 128) and k, v (B, N_keys, kv_heads * 128)."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (gate, "gate")):
-        if t is not None and t.dtype != torch.bfloat16:
-            raise TypeError(f"{n} must be bfloat16")
+    bf16 = torch.bfloat16
+    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or \
+            (gate is not None and gate.dtype is not bf16):
+        raise TypeError("q, k, v and gate must be bfloat16")
     if q.dim() != 3 or k.dim() != 3 or heads < 1 or q.shape[2] % heads:
         raise ValueError(f"q must be (B, N, heads * head_dim) with heads={heads}, k (B, N_keys, ...)")
     B, N, C = q.shape
     D = C // heads
-    Nk = k.shape[1]
-    if k.shape[0] != B or v.shape[:2] != k.shape[:2]:
+    ck = kv_heads * D
+    strides = (_token_stride(q, "q", C), _token_stride(k, "k", ck), _token_stride(v, "v", ck),
+               0 if gate is None else _token_stride(gate, "gate", C))
+    if k.shape != v.shape or k.shape[0] != B:
         raise ValueError("q, k and v must have one batch size, k and v one length")
     if gate is not None and gate.shape != q.shape:
         raise ValueError("gate must have q's shape")
-    ld = [_token_stride(t, n, w) for t, n, w in ((q, "q", C), (k, "k", kv_heads * D), (v, "v", kv_heads * D))]
-    ld.append(0 if gate is None else _token_stride(gate, "gate", C))
-    if lengths is not None and (lengths.dtype != torch.int32 or lengths.shape != (B,) or
-                                not lengths.is_contiguous()):
-        raise ValueError("lengths must be a contiguous int32 tensor (B,)")
+    at_lengths = None
+    if lengths is not None:
+        if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
+            raise ValueError("lengths must be a contiguous int32 tensor (B,)")
+        at_lengths = lengths.data_ptr()
     _same_device(q, k, v, gate, lengths)
-    return WindowShape(B, N, Nk, heads, kv_heads, D, *ld, window, sinks, block,
-                       None if lengths is None else lengths.data_ptr(), scale)
+    return WindowShape(B, N, k.shape[1], heads, kv_heads, D, *strides, window, sinks, block,
+                       at_lengths, scale)
 
 
 def window_anchor_fwd(q, k, v, gate, heads, kv_heads, window, sinks=0, block=1, lengths=None,
@@ -769,23 +781,26 @@ def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_hea
     and the window (bf16).  Position p lives in slot p while p < capacity, then in slot sinks + (p -
     sinks) % (capacity - sinks).  lengths (B,) int32 is left as it is; a negative one is an empty
     batch entry (nothing written, zeros out)."""
-    for t, n in ((q, "q"), (k, "k"), (v, "v"), (gate, "gate"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+    for t in (q, k, v, gate, k_cache, v_cache):
         if t is not None:
-            _need(t, n)
-            if t.dtype != torch.bfloat16:
-                raise TypeError(f"{n} must be bfloat16")
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("q, k, v, gate and the caches must be contiguous CUDA tensors")
+            if t.dtype is not torch.bfloat16:
+                raise TypeError("q, k, v, gate and the caches must be bfloat16")
     if q.dim() != 3 or k_cache.dim() != 3 or heads < 1 or q.shape[2] % heads:
         raise ValueError(f"q must be (B, N, heads * head_dim) with heads={heads}, caches (B, capacity, ...)")
     B, N, C = q.shape
     D = C // heads
-    if k.shape != (B, N, kv_heads * D) or v.shape != k.shape or (gate is not None and gate.shape != q.shape):
+    ck = kv_heads * D
+    if k.shape != (B, N, ck) or v.shape != k.shape or (gate is not None and gate.shape != q.shape):
         raise ValueError("k and v must be (B, N, kv_heads * head_dim), gate like q")
-    if k_cache.shape != (B, k_cache.shape[1], kv_heads * D) or v_cache.shape != k_cache.shape:
+    capacity = k_cache.shape[1]
+    if k_cache.shape != (B, capacity, ck) or v_cache.shape != k_cache.shape:
         raise ValueError("the caches must be (B, capacity, kv_heads * head_dim)")
-    if lengths.dtype != torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
+    if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be a contiguous int32 tensor (B,)")
     _same_device(q, k, v, gate, k_cache, v_cache, lengths, ws)
-    s = WindowDecodeShape(B, N, heads, kv_heads, D, k_cache.shape[1], window, sinks, scale)
+    s = WindowDecodeShape(B, N, heads, kv_heads, D, capacity, window, sinks, scale)
     out = _out_like(out, "out", q, C)
     if ws is None:
         ws = _ws(lib.sana_window_anchor_decode_workspace_size(s), q.device)

@@ -42,6 +42,11 @@ struct TileSpan {
   int ns, w0, w1;
   __device__ __forceinline__ bool has(int t) const { return t < ns || (t >= w0 && t <= w1); }
   __device__ __forceinline__ int count() const { return ns + (w1 >= w0 ? w1 - w0 + 1 : 0); }
+  // Columns of tile t that some row sees, a multiple of 32: of a tile outside the
+  // window only the sinks (a few tokens: the tile then costs a fraction).
+  __device__ __forceinline__ int width(int t, int sinks) const {
+    return t >= w0 ? kWinTile : min(kWinTile, (sinks - t * kWinTile + 31) & ~31);
+  }
 };
 __device__ __forceinline__ TileSpan window_span(const WindowDev& w, int p0, int p1, int len) {
   TileSpan s{0, 0, -1};

@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const TileSpan span = window_span(w, w.off + row0, w.off + min(row0 + kRows, w.N) - 1, len);
   const int steps = span.count();
   auto tile_of = [&](int t) { return t < span.ns ? t : span.w0 + t - span.ns; };
+  auto width_of = [&](int t) { return span.width(tile_of(t), w.sinks); };
   const WaitCtx wc{&ctl.abort_flag, status};
 
   if (tid == 0) {
@@ -654,28 +655,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMma) {
     if (steps > 0) {  // the whole warp, its elected lane issues
       const uint32_t lead = elect_lead();
-      const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, do V^T
+      const uint32_t idesc_s = idesc_bf16_f32(128, 0, 0, 0);  // Q K^T, do V^T; N by the tile's width
       const uint32_t idesc_g = idesc_bf16_f32(128, 128, 0, 1);  // dS K
       const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
       const uint64_t dd0 = smem_desc_sw128(smem_u32(do_s), 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), 16, 1024);
       const uint64_t mk0 = smem_desc_sw128(smem_u32(k_s), kHalf, 1024);
-      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bt) {  // D = A B^T
+      auto issue_ab = [&](uint32_t d, uint64_t a, uint64_t bt, int width) {  // D = A B^T over `width` keys
+        const uint32_t idesc = idesc_s | (uint32_t)(width >> 3) << 17;
         a = desc_local(a);
         bt = desc_local(bt);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_ss_lead(lead, d, desc_advance(a, o), desc_advance(bt, o), idesc_s, kk != 0);
+          umma_ss_lead(lead, d, desc_advance(a, o), desc_advance(bt, o), idesc, kk != 0);
         }
       };
       auto issue_s = [&](int t) {
-        issue_ab(tmem + (t & 1) * 128, dq0, desc_advance(dk0, (t % kDeep) * kTileB));
+        issue_ab(tmem + (t & 1) * 128, dq0, desc_advance(dk0, (t % kDeep) * kTileB), width_of(t));
         umma_commit_lead(lead, &ctl.s_full[t & 1]);
       };
       auto issue_dp = [&](int t) {
-        issue_ab(t_dp, dd0, desc_advance(dv0, (t % kShort) * kTileB));
+        issue_ab(t_dp, dd0, desc_advance(dv0, (t % kShort) * kTileB), width_of(t));
         umma_commit_lead(lead, &ctl.dp_full);
         umma_commit_lead(lead, &ctl.v_empty[t % kShort]);
       };
@@ -705,9 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           issue_dp(t + 1);
         }
         const uint64_t bm = desc_local(desc_advance(mk0, (t % kDeep) * kTileB));
+        const int ksteps = width_of(t) / 16;
 #pragma unroll
         for (int kk = 0; kk < kRows / 16; ++kk)
-          umma_ts_lead(lead, t_dq, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bm, kk * 2048),
+          if (kk < ksteps) umma_ts_lead(lead, t_dq, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bm, kk * 2048),
                        idesc_g, (t | kk) != 0);
         umma_commit_lead(lead, &ctl.dq_done);
         umma_commit_lead(lead, &ctl.k_empty[t % kDeep]);
@@ -743,6 +746,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // (a tile with dead rows is always masked)
       const bool masked = key0 + 32 > all_end || (key0 < all_low && key0 + 32 > w.sinks);
+      if (cg * 32 >= width_of(t)) {  // columns that no row of the tile sees were not made
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dp_full, t & 1, wc, 0xbd));
+        if (!ok) break;
+        mbar_arrive(&ctl.ds_full);
+        continue;
+      }
       uint32_t buf[32], pk[16];
       tmem_ld32(my_s, buf);
       tmem_ld_wait();

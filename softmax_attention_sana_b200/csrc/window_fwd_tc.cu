@@ -223,29 +223,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ MMA issuer
       if (span.n > 0) {  // the whole warp, its elected lane issues
         const uint32_t lead = elect_lead();
-        const uint32_t idesc_s = idesc_bf16_f32(128, 128, 0, 0);  // Q K^T, both K-major
+        const uint32_t idesc_s = idesc_bf16_f32(128, 0, 0, 0);  // Q K^T, both K-major; N by the tile's width
         const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
         const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
         int done[2] = {0, 0};  // P V products issued for each query tile
         auto issue_s = [&](int i, int u) {
+          const uint32_t idesc = idesc_s | (uint32_t)(span.s[i].width(span.tile(u), w.sinks) >> 3) << 17;
           const uint64_t a = desc_local(desc_advance(dq0, i * kTileB));
           const uint64_t bk = desc_local(desc_advance(dk0, (u % kKS) * kTileB));
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
             const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_ss_lead(lead, tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc_s, kk != 0);
+            umma_ss_lead(lead, tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc, kk != 0);
           }
           umma_commit_lead(lead, &ctl.s_full[i]);
         };
-        auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys
+        auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys, or what of them some row sees
+          const int steps = span.s[i].width(span.tile(u), w.sinks) / 16 - half * 4;
           const uint64_t bv = desc_local(desc_advance(dv0, (u % kVS) * kTileB + half * 8192));
           const uint32_t ap = tmem + i * 128 + half * 32;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts_lead(lead, tmem + 256 + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
-                         (done[i] | half | kk) != 0);
+            if (kk < steps)
+              umma_ts_lead(lead, tmem + 256 + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+                           (done[i] | half | kk) != 0);
         };
         bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
         if (ok) {
@@ -313,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = 0; ok && u < span.n; ++u) {
       if (!span.active(qi, u)) continue;
       const int key0 = span.tile(u) * kRows;
+      const int chunks = span.s[qi].width(span.tile(u), w.sinks) / 32;  // of 32 columns
       if (!__all_sync(0xffffffffu, mbar_wait(&ctl.s_full[qi], done & 1, wc, 0x98))) {
         ok = false;
         break;
@@ -321,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked = key0 + kRows > all_end || (key0 < all_low && key0 + kRows > w.sinks);
       uint32_t sc[4][32];  // the whole row
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tmem_s + lane_base + c * 32, sc[c]);
+      for (int c = 0; c < 4; ++c)
+        if (c < chunks) tmem_ld32(tmem_s + lane_base + c * 32, sc[c]);
       tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_tie(sc[c]);
@@ -345,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) top = chunk_max(sc[c], top);
+      for (int c = 0; c < 4; ++c)
+        if (c < chunks) top = chunk_max(sc[c], top);
       top *= sl;
       // The reference moves where the row's max passes it, on its first key or
       // by more than 2^16.  It is rounded up to an integer for the folded
@@ -401,25 +407,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        if (c < chunks) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float s0 = __uint_as_float(sc[c][i]), s1 = __uint_as_float(sc[c][i + 1]);
-          float p0, p1;
-          if (((i >> 1) & 7) >= 8 - kEmuPairs) {
-            exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
-          } else {
-            float x0, x1;
-            up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
-            p0 = ex2(x0);
-            p1 = ex2(x1);
+          for (int i = 0; i < 32; i += 2) {
+            const float s0 = __uint_as_float(sc[c][i]), s1 = __uint_as_float(sc[c][i + 1]);
+            float p0, p1;
+            if (((i >> 1) & 7) >= 8 - kEmuPairs) {
+              exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
+            } else {
+              float x0, x1;
+              up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
+              p0 = ex2(x0);
+              p1 = ex2(x1);
+            }
+            rs2 = add2(rs2, pk2(p0, p1));
+            pk[i / 2] = f2_to_bf2(p0, p1);
           }
-          rs2 = add2(rs2, pk2(p0, p1));
-          pk[i / 2] = f2_to_bf2(p0, p1);
+          // over S columns that are in registers; after each half of the keys the
+          // product with V may start on it
+          tmem_st16(tmem_s + lane_base + c * 16, pk);
         }
-        // over S columns that are in registers; after each half of the keys the
-        // product with V may start on it
-        tmem_st16(tmem_s + lane_base + c * 16, pk);
         if (c & 1) {
           tmem_st_wait();
           tc_fence_before();
