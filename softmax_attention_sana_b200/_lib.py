@@ -558,6 +558,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _ws_args(ws, t):
+    """Address and bytes of a caller's workspace for a call on t."""
+    _need(ws, "ws")
+    _same_device(t, ws)
+    return ws.data_ptr(), ws.nbytes
+
+
 def _token_stride(t, name, width):
     """Elements between the tokens of a (B, N, width) tensor whose rows are contiguous and whose
     sequences follow each other at the same stride (a slice of a packed projection is one)."""
@@ -681,10 +688,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv
     dwk = None if k is None else torch.empty_like(dwq)
     if ws is None:
         ws = _ws(lib.sana_qk_norm_rope_bwd_workspace_size(ctypes.byref(s)), q.device)
-    _same_device(q, ws)
     _call_on(q, lib.sana_qk_norm_rope_bwd, s, _dtype_code(q), at, q.data_ptr(), _addr(k),
              _addr(q_weight), _addr(k_weight), eps, q_mul, dq_out.data_ptr(), _addr(dk_out),
-             dq.data_ptr(), _addr(dk), dwq.data_ptr(), _addr(dwk), ws.data_ptr(), ws.numel())
+             dq.data_ptr(), _addr(dk), dwq.data_ptr(), _addr(dwk), *_ws_args(ws, q))
     return dq, dk, dwq, dwk
 
 
@@ -761,10 +767,9 @@ def window_anchor_bwd(q, k, v, gate, out, lse, dy, heads, kv_heads, window, sink
         return dq, dk.zero_(), dv.zero_(), dg
     if ws is None:
         ws = _ws(lib.sana_window_anchor_bwd_workspace_size(ctypes.byref(s), int(gate is not None)), q.device)
-    _same_device(q, ws)
     _call_on(q, lib.sana_window_anchor_bwd, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              _addr(gate), out.data_ptr(), lse.data_ptr(), dy.data_ptr(), dq.data_ptr(),
-             dk.data_ptr(), dv.data_ptr(), _addr(dg), ws.data_ptr(), ws.numel())
+             dk.data_ptr(), dv.data_ptr(), _addr(dg), *_ws_args(ws, q))
     return dq, dk, dv, dg
 
 
@@ -799,14 +804,14 @@ def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_hea
         raise ValueError("the caches must be (B, capacity, kv_heads * head_dim)")
     if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be a contiguous int32 tensor (B,)")
-    _same_device(q, k, v, gate, k_cache, v_cache, lengths, ws)
+    _same_device(q, k, v, gate, k_cache, v_cache, lengths)
     s = WindowDecodeShape(B, N, heads, kv_heads, D, capacity, window, sinks, scale)
     out = _out_like(out, "out", q, C)
     if ws is None:
         ws = _ws(lib.sana_window_anchor_decode_workspace_size(s), q.device)
     _call_on(q, lib.sana_window_anchor_decode, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              _addr(gate), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
-             out.data_ptr(), ws.data_ptr(), ws.numel())
+             out.data_ptr(), *_ws_args(ws, q))
     return out
 
 

@@ -177,10 +177,11 @@ __device__ __forceinline__ QSpan query_span(const WindowDev& w, int kt, int len)
   return s;
 }
 
-// How the host cut the work: key tiles [0, sink_tiles) into sink_parts shares
-// each, the others into win_parts, of `chunk` (query head, query tile) steps.
+// How the host cut the work: key tiles [0, sink_tiles) into sink_parts shares of
+// sink_chunk (query head, query tile) steps each, the others into win_parts of
+// win_chunk.
 struct DkvPlan {
-  int tiles, sink_tiles, sink_parts, win_parts, chunk;
+  int tiles, sink_tiles, sink_parts, sink_chunk, win_parts, win_chunk;
 };
 
 struct DkvCtl {
@@ -228,13 +229,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int len = window_length(w, b);
   const QSpan qs = query_span(w, kt, len);
-  const int step0 = share * plan.chunk;
-  const int steps = max(0, min(group * qs.count - step0, plan.chunk));
+  const int chunk = kt < plan.sink_tiles ? plan.sink_chunk : plan.win_chunk;
+  const int step0 = share * chunk;
+  const int steps = max(0, min(group * qs.count - step0, chunk));
   const WaitCtx wc{&ctl.abort_flag, status};
   auto head_of = [&](int t) { return hk * group + (step0 + t) / qs.count; };
   auto qrow_of = [&](int t) { return (qs.first + (step0 + t) % qs.count) * kRows; };
 
-  if (tid == 0) {
+  auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+    tma_load_3d(dst, map, bar, head * kD, row, b);
+    tma_load_3d(dst + kHalf, map, bar, head * kD + 64, row, b);
+  };
+  auto load_q = [&](int t) {
+    const int st = t % kDeep;
+    mbar_arrive_expect_tx(&ctl.q_full[st], kTileB);
+    load_tile(q_s + st * kTileB, &tm_q, &ctl.q_full[st], head_of(t), qrow_of(t));
+  };
+  auto load_do = [&](int t) {
+    const int st = t % kShort, h = head_of(t), row = qrow_of(t);
+    const size_t at = ((size_t)b * w.heads + h) * n_pad + row;
+    mbar_arrive_expect_tx(&ctl.do_full[st], kTileB + 2 * kRows * 4);
+    load_tile(do_s + st * kTileB, &tm_do, &ctl.do_full[st], h, row);
+    bulk_load(stat + st * 2 * kRows, nlse + at, kRows * 4, &ctl.do_full[st]);
+    bulk_load(stat + st * 2 * kRows + kRows, ndelta + at, kRows * 4, &ctl.do_full[st]);
+  };
+  if (warp == kWarpProd && lane == 0) {
     mbar_init(&ctl.kv_full, 1);
     for (int i = 0; i < kDeep; ++i) {
       mbar_init(&ctl.q_full[i], 1);
@@ -252,6 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl.dk_done, 1);
     ctl.abort_flag = 0;
     mbar_fence_init();
+    if (steps > 0) {  // the first loads run while the rest of the CTA sets up
+      mbar_arrive_expect_tx(&ctl.kv_full, 2 * kTileB);
+      load_tile(k_s, &tm_k, &ctl.kv_full, hk, kt * kRows);
+      load_q(0);
+      load_tile(v_s, &tm_v, &ctl.kv_full, hk, kt * kRows);
+      load_do(0);
+    }
   }
   if (warp == kWarpMma) {
     tmem_alloc(&ctl.tmem, 512);
@@ -265,30 +291,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpProd) {
     if (lane == 0 && steps > 0) {
-      mbar_arrive_expect_tx(&ctl.kv_full, 2 * kTileB);
-      tma_load_3d(k_s, &tm_k, &ctl.kv_full, hk * kD, kt * kRows, b);
-      tma_load_3d(k_s + kHalf, &tm_k, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
-      tma_load_3d(v_s, &tm_v, &ctl.kv_full, hk * kD, kt * kRows, b);
-      tma_load_3d(v_s + kHalf, &tm_v, &ctl.kv_full, hk * kD + 64, kt * kRows, b);
-      int nq = 0, nd = 0;
-      for (int t = 0; t < steps; ++t) {
-        const int sq = t % kDeep, sd = t % kShort, h = head_of(t), row = qrow_of(t);
-        if (t >= kDeep && !mbar_wait(&ctl.q_empty[sq], ((t / kDeep) - 1) & 1, wc, 0xa1)) break;
-        mbar_arrive_expect_tx(&ctl.q_full[sq], kTileB);
-        tma_load_3d(q_s + sq * kTileB, &tm_q, &ctl.q_full[sq], h * kD, row, b);
-        tma_load_3d(q_s + sq * kTileB + kHalf, &tm_q, &ctl.q_full[sq], h * kD + 64, row, b);
+      int nq = 1, nd = 1;
+      for (int t = 1; t < steps; ++t) {
+        if (t >= kDeep && !mbar_wait(&ctl.q_empty[t % kDeep], ((t / kDeep) - 1) & 1, wc, 0xa1)) break;
+        load_q(t);
         ++nq;
         // a do slot is free once dV has read it, its statistics' slot once dS is
         // made, which dK's end (q_empty) implies
-        if (t >= kShort && (!mbar_wait(&ctl.do_empty[sd], ((t / kShort) - 1) & 1, wc, 0xab) ||
+        if (t >= kShort && (!mbar_wait(&ctl.do_empty[t % kShort], ((t / kShort) - 1) & 1, wc, 0xab) ||
                             !mbar_wait(&ctl.q_empty[(t - kShort) % kDeep], ((t - kShort) / kDeep) & 1, wc, 0xb0)))
           break;
-        const size_t at = ((size_t)b * w.heads + h) * n_pad + row;
-        mbar_arrive_expect_tx(&ctl.do_full[sd], kTileB + 2 * kRows * 4);
-        tma_load_3d(do_s + sd * kTileB, &tm_do, &ctl.do_full[sd], h * kD, row, b);
-        tma_load_3d(do_s + sd * kTileB + kHalf, &tm_do, &ctl.do_full[sd], h * kD + 64, row, b);
-        bulk_load(stat + sd * 2 * kRows, nlse + at, kRows * 4, &ctl.do_full[sd]);
-        bulk_load(stat + sd * 2 * kRows + kRows, ndelta + at, kRows * 4, &ctl.do_full[sd]);
+        load_do(t);
         ++nd;
       }
       if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
@@ -546,7 +559,8 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4)
   const int item = sink ? kt * plan.sink_parts
                         : plan.sink_tiles * plan.sink_parts + (kt - plan.sink_tiles) * plan.win_parts;
   const QSpan qs = query_span(w, kt, window_length(w, b));
-  const int n = (w.heads / w.kv_heads * qs.count + plan.chunk - 1) / plan.chunk;  // shares written
+  const int chunk = sink ? plan.sink_chunk : plan.win_chunk;
+  const int n = (w.heads / w.kv_heads * qs.count + chunk - 1) / chunk;  // shares written
   const int i = slice * kJoinRows * (kD / 4) + threadIdx.x, j = kt * kRows + i / (kD / 4);
   if (j >= w.N_keys) return;
   const float4* p = reinterpret_cast<const float4*>(
@@ -597,7 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto width_of = [&](int t) { return span.width(tile_of(t), w.sinks); };
   const WaitCtx wc{&ctl.abort_flag, status};
 
-  if (tid == 0) {
+  auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+    tma_load_3d(dst, map, bar, head * kD, row, b);
+    tma_load_3d(dst + kHalf, map, bar, head * kD + 64, row, b);
+  };
+  auto load_k = [&](int t) {
+    const int st = t % kDeep;
+    mbar_arrive_expect_tx(&ctl.k_full[st], kTileB);
+    load_tile(k_s + st * kTileB, &tm_k, &ctl.k_full[st], hk, tile_of(t) * kRows);
+  };
+  auto load_v = [&](int t) {
+    const int st = t % kShort;
+    mbar_arrive_expect_tx(&ctl.v_full[st], kTileB);
+    load_tile(v_s + st * kTileB, &tm_v, &ctl.v_full[st], hk, tile_of(t) * kRows);
+  };
+  if (warp == kWarpProd && lane == 0) {
     mbar_init(&ctl.q_full, 1);
     for (int i = 0; i < kDeep; ++i) {
       mbar_init(&ctl.k_full[i], 1);
@@ -614,6 +642,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl.dq_done, 1);
     ctl.abort_flag = 0;
     mbar_fence_init();
+    if (steps > 0) {  // the first loads run while the rest of the CTA sets up
+      mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
+      load_tile(q_s, &tm_q, &ctl.q_full, h, row0);
+      load_k(0);
+      load_tile(do_s, &tm_do, &ctl.q_full, h, row0);
+      load_v(0);
+    }
   }
   if (warp == kWarpMma) {
     tmem_alloc(&ctl.tmem, 512);
@@ -627,23 +662,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpProd) {
     if (lane == 0 && steps > 0) {
-      mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
-      tma_load_3d(q_s, &tm_q, &ctl.q_full, h * kD, row0, b);
-      tma_load_3d(q_s + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0, b);
-      tma_load_3d(do_s, &tm_do, &ctl.q_full, h * kD, row0, b);
-      tma_load_3d(do_s + kHalf, &tm_do, &ctl.q_full, h * kD + 64, row0, b);
-      int nk = 0, nv = 0;
-      for (int t = 0; t < steps; ++t) {
-        const int sk = t % kDeep, sv = t % kShort, row = tile_of(t) * kRows;
-        if (t >= kDeep && !mbar_wait(&ctl.k_empty[sk], ((t / kDeep) - 1) & 1, wc, 0xb1)) break;
-        mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
-        tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
-        tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
+      int nk = 1, nv = 1;
+      for (int t = 1; t < steps; ++t) {
+        if (t >= kDeep && !mbar_wait(&ctl.k_empty[t % kDeep], ((t / kDeep) - 1) & 1, wc, 0xb1)) break;
+        load_k(t);
         ++nk;
-        if (t >= kShort && !mbar_wait(&ctl.v_empty[sv], ((t / kShort) - 1) & 1, wc, 0xbb)) break;
-        mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
-        tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
-        tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
+        if (t >= kShort && !mbar_wait(&ctl.v_empty[t % kShort], ((t / kShort) - 1) & 1, wc, 0xbb)) break;
+        load_v(t);
         ++nv;
       }
       if (*wc.abort_flag) {
@@ -841,10 +866,11 @@ static_assert(kDkvSmem + sizeof(DkvCtl) <= kSmemMax && kDqSmem + sizeof(DqCtl) <
 
 // A key tile is left whole while there are two CTAs for every SM; otherwise its
 // steps are cut so that there are, down to four steps each.  The sinks' tiles,
-// which all later queries see, are cut into shares as long as a window tile's.
+// which all later queries see, are cut into shares as long as a window tile's, or
+// longer where that would make more of them than four for every SM.
 DkvPlan dkv_plan(const WindowCall& c) {
   DkvPlan p{};
-  const int group = c.heads / c.kv_heads;
+  const long long group = c.heads / c.kv_heads;
   const long long q_tiles = (c.N + kRows - 1) / kRows;
   p.tiles = (c.N_keys + kRows - 1) / kRows;
   // query tiles that a key tile's window can reach
@@ -855,14 +881,17 @@ DkvPlan dkv_plan(const WindowCall& c) {
     p.sink_tiles = (c.sinks + kRows - 1) / kRows;
     if (p.sink_tiles > p.tiles) p.sink_tiles = p.tiles;
   }
-  const long long base = group * reach;
-  const long long ctas = (long long)p.tiles * c.kv_heads * c.B;
+  const long long base = group * reach, columns = (long long)c.kv_heads * c.B;
+  const long long ctas = p.tiles * columns;
   const long long parts = ctas >= 2 * kNumSMs ? 1 : (2 * kNumSMs + ctas - 1) / ctas;
   long long chunk = (base + parts - 1) / parts;
   if (chunk < 4) chunk = 4;
-  p.chunk = (int)chunk;
+  p.win_chunk = (int)chunk;
   p.win_parts = (int)((base + chunk - 1) / chunk);
-  p.sink_parts = (int)((group * q_tiles + chunk - 1) / chunk);
+  const long long sink_steps = group * q_tiles, most = sink_steps * p.sink_tiles * columns / (4 * kNumSMs) + 1;
+  if (chunk < most) chunk = most;
+  p.sink_chunk = (int)chunk;
+  p.sink_parts = (int)((sink_steps + chunk - 1) / chunk);
   return p;
 }
 int dkv_items(const DkvPlan& p) {

@@ -8,15 +8,17 @@
 // to bf16 as the A operand of P V: each rounding is 2^-9 of its term and they
 // average out).
 //
-// One CTA per (batch, query head, pair of 128-query tiles); the two tiles share
-// the K and V tiles in shared memory, and their softmax warpgroups alternate
-// with the tensor core:
-//   producer warp : TMA Q_0, Q_1 once; K_u, V_u in two-stage rings over the key
-//                   tiles that either query tile sees (sinks, then the window);
-//                   the gate at the end, into the K ring
+// One CTA per (batch, query head, kQ 128-query tiles).  With two query tiles they
+// share the K and V tiles in shared memory and their softmax warpgroups alternate
+// with the tensor core; with one, two CTAs share an SM, alternate the same way,
+// and one's start and end run under the other's loop, at twice the K and V
+// traffic: the form for short windows.
+//   producer warp : TMA Q_i once; K_u, V_u in rings of kQ stages over the key
+//                   tiles that any query tile sees (sinks, then the window); the
+//                   gate at the end, into the K ring
 //   MMA warp      : for each of them, where query tile i sees it: O_i += P_i V,
 //                   and S_i = Q_i K^T of the next one
-//   2 x 4 softmax warps (thread = query row): the score row in registers, masked
+//   kQ x 4 softmax warps (thread = query row): the score row in registers, masked
 //                   where some row of the query tile sees the key tile in part;
 //                   row max, lazy rescaling of O in TMEM (where a max passes the
 //                   reference by more than 2^16), exponentials, P over its S
@@ -24,7 +26,7 @@
 //                   1/l, gate, lse and the TMA store.
 // Registers: a softmax thread holds 128 scores, more than the 168 registers of
 // an even share, so the other warps give some of theirs up.
-// TMEM (512 columns): S_0 S_1 O_0 O_1, 128 each; P_i over the first half of S_i.
+// TMEM: S_i, then O_i, 128 columns each; P_i over the first half of S_i.
 //
 // Bound by the tensor core (4 * 128 flops per pair and head) with the MUFU unit
 // close behind: a quarter of the exponentials run as a cubic on the FMA pipe.
@@ -41,14 +43,28 @@ constexpr int kD = 128;
 constexpr int kRows = kWinTile;
 constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
 constexpr int kTileB = 2 * kHalf;      // 32 KB
-constexpr int kKS = 2, kVS = 2;        // K and V stages
-constexpr int kThreads = 384;          // 8 softmax warps, producer, MMA, two idle warps
-constexpr int kWarpProd = 8, kWarpMma = 9;
-// Registers a thread: 168 at launch; the softmax warps take more from the others.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
-static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "more registers than at launch");
+// Shape of a CTA with kQ query tiles: 4 kQ softmax warps, producer, MMA, two idle
+// warps; kQ stages of K and V.  Registers a thread: the softmax warps take more
+// than an even share from the others (3 - kQ CTAs on an SM).
+template <int kQ>
+struct Form {
+  static constexpr int kThreads = 128 * kQ + 128;
+  static constexpr int kWarpProd = 4 * kQ, kWarpMma = 4 * kQ + 1;
+  static constexpr int kStages = kQ;
+  static constexpr int kLaunchRegs = kQ == 2 ? 168 : 128;
+  static constexpr int kRegsSoftmax = kQ == 2 ? 216 : 208, kRegsOther = kQ == 2 ? 72 : 48;
+  static_assert(128 * kQ * kRegsSoftmax + 128 * kRegsOther <= kThreads * kLaunchRegs, "more registers than at launch");
+  static constexpr int kTmemCols = 256 * kQ;
+  static constexpr size_t kSmem = 1024 + 3 * kQ * (size_t)kTileB;
+};
 constexpr float kRescaleLog2 = 16.f;
-constexpr int kEmuPairs = 2;           // of every 8 pairs of exponentials, on the FMA pipe
+// Query tiles that see at most this many key tiles run one to a CTA.  16384 rows
+// of 16 heads, one against two: window 256 (4 tiles) 92 against 111 us, 1024 (10
+// tiles) 177 against 190 us, 4096 (34 tiles) 486 against 477 us; 32 heads on 8 key
+// heads with a gate: 210 against 244, 411 against 419, 1027 against 991 us.
+constexpr int kSingleReach = 10;
+// Of every 8 pairs of exponentials, on the FMA pipe (none: 493 us at window 4096, one 486, two 477, three 478).
+constexpr int kEmuPairs = 2;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^(sl * s - m) for two scores on the FMA pipe, m an integer below 2^22 in
@@ -76,30 +92,33 @@ __device__ __forceinline__ void exp2_scaled2(float s0, float s1, float s_lo, uin
   y1 = __uint_as_float(r1);
 }
 
+template <int kQ>
 struct WinCtl {
   uint64_t q_full, g_full;
-  uint64_t k_full[kKS], k_empty[kKS];
-  uint64_t v_full[kVS], v_empty[kVS];
-  uint64_t s_full[2], p_full[2][2], pv_done[2];  // p_full[tile][half of the keys]
-  uint64_t ysync[2];
+  uint64_t k_full[kQ], k_empty[kQ];
+  uint64_t v_full[kQ], v_empty[kQ];
+  uint64_t s_full[kQ], p_full[kQ][2], pv_done[kQ];  // p_full[tile][half of the keys]
+  uint64_t ysync[kQ];
   uint32_t tmem;
   int abort_flag;
 };
 
-// The key tiles of a CTA: those that either query tile sees, sinks first.
-struct PairSpan {
-  TileSpan s[2];
+// The key tiles of a CTA: those that any of its query tiles sees, sinks first.
+template <int kQ>
+struct CtaSpan {
+  TileSpan s[kQ];
   int ns, w0, n;
   __device__ __forceinline__ int tile(int u) const { return u < ns ? u : w0 + (u - ns); }
   __device__ __forceinline__ bool active(int i, int u) const { return u < n && s[i].has(tile(u)); }
 };
-__device__ __forceinline__ PairSpan pair_span(const WindowDev& w, int row0, int len) {
-  PairSpan p;
+template <int kQ>
+__device__ __forceinline__ CtaSpan<kQ> cta_span(const WindowDev& w, int row0, int len) {
+  CtaSpan<kQ> p;
   int last = -1;
   p.w0 = 0x7fffffff;
   p.ns = 0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kQ; ++i) {
     const int a = row0 + i * kRows, b = min(a + kRows, w.N) - 1;
     p.s[i] = window_span(w, w.off + a, w.off + b, len);
     if (p.s[i].w1 >= p.s[i].w0) {
@@ -113,40 +132,54 @@ __device__ __forceinline__ PairSpan pair_span(const WindowDev& w, int row0, int 
   return p;
 }
 
-template <bool kGate>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kQ, bool kGate>
+__global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
                       const __grid_constant__ CUtensorMap tm_y, const WindowDev w, float sl,
                       float* __restrict__ lse, int* status) {
+  using F = Form<kQ>;
+  constexpr int kStages = F::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ WinCtl ctl;
+  __shared__ WinCtl<kQ> ctl;
   uint8_t* smem = align1024(smem_raw);
-  uint8_t* q_s = smem;                // Q_0, Q_1 (later: Y staging)
-  uint8_t* k_s = q_s + 2 * kTileB;    // K ring (later: gate tiles)
-  uint8_t* v_s = k_s + kKS * kTileB;  // V ring
+  uint8_t* q_s = smem;                    // Q_i (later: Y staging)
+  uint8_t* k_s = q_s + kQ * kTileB;       // K ring (later: gate tiles)
+  uint8_t* v_s = k_s + kStages * kTileB;  // V ring
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the last query tiles see the most keys where the window is open: they start first
   const int qp = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (w.heads / w.kv_heads);
-  const int row0 = qp * 2 * kRows;
+  const int row0 = qp * kQ * kRows;
   const int len = window_length(w, b);
-  const PairSpan span = pair_span(w, row0, len);
+  const CtaSpan<kQ> span = cta_span<kQ>(w, row0, len);
   const WaitCtx wc{&ctl.abort_flag, status};
 
-  if (tid == 0) {
+  auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+    tma_load_3d(dst, map, bar, head * kD, row, b);
+    tma_load_3d(dst + kHalf, map, bar, head * kD + 64, row, b);
+  };
+  auto load_k = [&](int u) {
+    const int st = u % kStages;
+    mbar_arrive_expect_tx(&ctl.k_full[st], kTileB);
+    load_tile(k_s + st * kTileB, &tm_k, &ctl.k_full[st], hk, span.tile(u) * kRows);
+  };
+  auto load_v = [&](int u) {
+    const int st = u % kStages;
+    mbar_arrive_expect_tx(&ctl.v_full[st], kTileB);
+    load_tile(v_s + st * kTileB, &tm_v, &ctl.v_full[st], hk, span.tile(u) * kRows);
+  };
+  if (warp == F::kWarpProd && lane == 0) {
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.g_full, 1);
-    for (int i = 0; i < kKS; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&ctl.k_full[i], 1);
       mbar_init(&ctl.k_empty[i], 1);
-    }
-    for (int i = 0; i < kVS; ++i) {
       mbar_init(&ctl.v_full[i], 1);
       mbar_init(&ctl.v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kQ; ++i) {
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_full[i][0], 128);
       mbar_init(&ctl.p_full[i][1], 128);
@@ -155,9 +188,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ctl.abort_flag = 0;
     mbar_fence_init();
+    if (span.n > 0) {  // the first loads run while the rest of the CTA sets up
+      mbar_arrive_expect_tx(&ctl.q_full, kQ * kTileB);
+      for (int i = 0; i < kQ; ++i)  // a tile past N reads as zeros
+        load_tile(q_s + i * kTileB, &tm_q, &ctl.q_full, h, row0 + i * kRows);
+      for (int u = 0; u < min(span.n, kStages); ++u) {
+        load_k(u);
+        load_v(u);
+      }
+    }
   }
-  if (warp == kWarpMma) {
-    tmem_alloc(&ctl.tmem, 512);
+  if (warp == F::kWarpMma) {
+    tmem_alloc(&ctl.tmem, F::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -165,61 +207,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
 
-  if (warp >= kWarpProd) {
-    warpgroup_regs_dec<kRegsOther>();
-    if (warp == kWarpProd) {
+  if (warp >= F::kWarpProd) {
+    warpgroup_regs_dec<F::kRegsOther>();
+    if (warp == F::kWarpProd) {
       // ------------------------------------------------ TMA producer
       if (lane == 0 && span.n > 0) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
-        mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
-        for (int i = 0; i < 2; ++i) {  // a tile past N reads as zeros
-          tma_load_3d(q_s + i * kTileB, &tm_q, &ctl.q_full, h * kD, row0 + i * kRows, b);
-          tma_load_3d(q_s + i * kTileB + kHalf, &tm_q, &ctl.q_full, h * kD + 64, row0 + i * kRows, b);
-        }
-        int nk = 0, nv = 0;
+        int nk = min(span.n, kStages), nv = nk;  // loads so far
         bool ok = true;
-        for (int u = 0; u < span.n; ++u) {
-          const int sk = u % kKS, sv = u % kVS;
-          const int row = span.tile(u) * kRows;
-          if (u >= kKS && !mbar_wait(&ctl.k_empty[sk], ((u / kKS) - 1) & 1, wc, 0x91)) {
+        for (int u = kStages; u < span.n; ++u) {
+          if (!mbar_wait(&ctl.k_empty[u % kStages], ((u / kStages) - 1) & 1, wc, 0x91)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&ctl.k_full[sk], kTileB);
-          tma_load_3d(k_s + sk * kTileB, &tm_k, &ctl.k_full[sk], hk * kD, row, b);
-          tma_load_3d(k_s + sk * kTileB + kHalf, &tm_k, &ctl.k_full[sk], hk * kD + 64, row, b);
+          load_k(u);
           ++nk;
-          if (u >= kVS && !mbar_wait(&ctl.v_empty[sv], ((u / kVS) - 1) & 1, wc, 0x92)) {
+          if (!mbar_wait(&ctl.v_empty[u % kStages], ((u / kStages) - 1) & 1, wc, 0x92)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&ctl.v_full[sv], kTileB);
-          tma_load_3d(v_s + sv * kTileB, &tm_v, &ctl.v_full[sv], hk * kD, row, b);
-          tma_load_3d(v_s + sv * kTileB + kHalf, &tm_v, &ctl.v_full[sv], hk * kD + 64, row, b);
+          load_v(u);
           ++nv;
         }
         // the gate goes into the K ring once the last S products have read it
         if (ok && kGate) {
-          for (int u = (span.n > kKS ? span.n - kKS : 0); u < span.n && ok; ++u)
-            ok = mbar_wait(&ctl.k_empty[u % kKS], (u / kKS) & 1, wc, 0x9c);
+          for (int u = max(span.n - kStages, 0); u < span.n && ok; ++u)
+            ok = mbar_wait(&ctl.k_empty[u % kStages], (u / kStages) & 1, wc, 0x9c);
           if (ok) {
-            mbar_arrive_expect_tx(&ctl.g_full, 2 * kTileB);
-            for (int i = 0; i < 2; ++i) {
-              tma_load_3d(k_s + i * kTileB, &tm_g, &ctl.g_full, h * kD, row0 + i * kRows, b);
-              tma_load_3d(k_s + i * kTileB + kHalf, &tm_g, &ctl.g_full, h * kD + 64, row0 + i * kRows, b);
-            }
+            mbar_arrive_expect_tx(&ctl.g_full, kQ * kTileB);
+            for (int i = 0; i < kQ; ++i) load_tile(k_s + i * kTileB, &tm_g, &ctl.g_full, h, row0 + i * kRows);
           }
         }
         if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
           mbar_drain(&ctl.q_full, 0);
-          for (int u = nk > kKS ? nk - kKS : 0; u < nk; ++u) mbar_drain(&ctl.k_full[u % kKS], (u / kKS) & 1);
-          for (int u = nv > kVS ? nv - kVS : 0; u < nv; ++u) mbar_drain(&ctl.v_full[u % kVS], (u / kVS) & 1);
+          for (int u = max(nk - kStages, 0); u < nk; ++u) mbar_drain(&ctl.k_full[u % kStages], (u / kStages) & 1);
+          for (int u = max(nv - kStages, 0); u < nv; ++u) mbar_drain(&ctl.v_full[u % kStages], (u / kStages) & 1);
           if (ok && kGate) mbar_drain(&ctl.g_full, 0);
         }
       }
-    } else if (warp == kWarpMma) {
+    } else if (warp == F::kWarpMma) {
       // ------------------------------------------------ MMA issuer
       if (span.n > 0) {  // the whole warp, its elected lane issues
         const uint32_t lead = elect_lead();
@@ -228,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
-        int done[2] = {0, 0};  // P V products issued for each query tile
+        int done[kQ] = {};  // P V products issued for each query tile
         auto issue_s = [&](int i, int u) {
           const uint32_t idesc = idesc_s | (uint32_t)(span.s[i].width(span.tile(u), w.sinks) >> 3) << 17;
           const uint64_t a = desc_local(desc_advance(dq0, i * kTileB));
-          const uint64_t bk = desc_local(desc_advance(dk0, (u % kKS) * kTileB));
+          const uint64_t bk = desc_local(desc_advance(dk0, (u % kStages) * kTileB));
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
             const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
@@ -242,26 +267,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys, or what of them some row sees
           const int steps = span.s[i].width(span.tile(u), w.sinks) / 16 - half * 4;
-          const uint64_t bv = desc_local(desc_advance(dv0, (u % kVS) * kTileB + half * 8192));
+          const uint64_t bv = desc_local(desc_advance(dv0, (u % kStages) * kTileB + half * 8192));
           const uint32_t ap = tmem + i * 128 + half * 32;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps)
-              umma_ts_lead(lead, tmem + 256 + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+              umma_ts_lead(lead, tmem + (kQ + i) * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
                            (done[i] | half | kk) != 0);
         };
         bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
         if (ok) {
           tc_fence_after();
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < kQ; ++i)
             if (span.active(i, 0)) issue_s(i, 0);
           umma_commit_lead(lead, &ctl.k_empty[0]);
         }
         for (int u = 0; ok && u < span.n; ++u) {
           const bool more = u + 1 < span.n;
-          if (!mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x95)) break;
-          if (more && !mbar_wait(&ctl.k_full[(u + 1) % kKS], ((u + 1) / kKS) & 1, wc, 0x96)) break;
-          for (int i = 0; i < 2; ++i) {
+          if (!mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x95)) break;
+          if (more && !mbar_wait(&ctl.k_full[(u + 1) % kStages], ((u + 1) / kStages) & 1, wc, 0x96)) break;
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
             if (span.active(i, u)) {
               // P_i is in TMEM, half by half, and O_i has been rescaled if needed
               for (int half = 0; half < 2; ++half) {
@@ -287,18 +313,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          umma_commit_lead(lead, &ctl.v_empty[u % kVS]);
-          if (more) umma_commit_lead(lead, &ctl.k_empty[(u + 1) % kKS]);
+          umma_commit_lead(lead, &ctl.v_empty[u % kStages]);
+          if (more) umma_commit_lead(lead, &ctl.k_empty[(u + 1) % kStages]);
         }
       }
     }
   } else {
     // ------------------------------------------------ softmax warps: thread = query row
-    warpgroup_regs_inc<kRegsSoftmax>();
-    const int qi = warp >> 2;
+    warpgroup_regs_inc<F::kRegsSoftmax>();
+    const int qi = kQ == 1 ? 0 : warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tmem_s = tmem + qi * 128, tmem_o = tmem + 256 + qi * 128;
+    const uint32_t tmem_s = tmem + qi * 128, tmem_o = tmem + (kQ + qi) * 128;
     const int row = row0 + qi * kRows + r;
     const int pos = w.off + row;
     const bool row_live = row < w.N && pos < len;
@@ -393,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tail) {
         // padding rows of V meet P = 0: zero them, whatever they hold (both
         // warpgroups write the same zeros before their own product reads V)
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kVS], (u / kVS) & 1, wc, 0x9d))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
           ok = false;
           break;
         }
-        uint8_t* vt = v_s + (u % kVS) * kTileB;
+        uint8_t* vt = v_s + (u % kStages) * kTileB;
         if (key0 + r >= len) {
 #pragma unroll
           for (int c = 0; c < 16; ++c)
@@ -493,49 +519,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_store_3d(&tm_y, ybuf, h * kD, row0 + qi * kRows, b);
       tma_store_3d(&tm_y, ybuf + kHalf, h * kD + 64, row0 + qi * kRows, b);
       bulk_commit();
-      bulk_wait0();
+      bulk_wait_read0();  // the staging may go; the grid's end makes the rows visible
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == F::kWarpMma) {
     if (*wc.abort_flag) {  // MMAs in flight finish before TMEM is freed
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kQ; ++i) {
         const int n = span.s[i].count();
         if (n) mbar_drain(&ctl.pv_done[i], (n - 1) & 1);
       }
     }
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, F::kTmemCols);
   }
 }
 
-constexpr size_t kWinSmem = 1024 + 2 * kTileB + kKS * kTileB + kVS * kTileB;
+template <int kQ, bool kGate>
+void launch(const CUtensorMap* t, const WindowDev& w, int B, float sl, float* lse, cudaStream_t st) {
+  const dim3 grid((w.N + kQ * kRows - 1) / (kQ * kRows), w.heads, B);
+  window_fwd_kernel<kQ, kGate><<<grid, Form<kQ>::kThreads, Form<kQ>::kSmem, st>>>(t[0], t[1], t[2], t[3], t[4], w, sl,
+                                                                                lse, status_word());
+}
+template <int kQ, bool kGate>
+void allow_smem() {
+  cudaFuncSetAttribute(window_fwd_kernel<kQ, kGate>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Form<kQ>::kSmem);
+}
 
 }  // namespace
 
 sana_status window_fwd_run(const WindowCall& c, float* lse, void* out, cudaStream_t st) {
   const uint64_t N = c.N, Nk = c.N_keys, C = (uint64_t)c.heads * kD, Ck = (uint64_t)c.kv_heads * kD;
-  CUtensorMap tq, tk, tv, tg, ty;
-  bool okm = make_tmap_bf16_3d(&tq, c.q, C, N, c.B, c.q_stride, N * c.q_stride, kRows) &&
-             make_tmap_bf16_3d(&tk, c.k, Ck, Nk, c.B, c.k_stride, Nk * c.k_stride, kRows) &&
-             make_tmap_bf16_3d(&tv, c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows) &&
-             make_tmap_bf16_3d(&ty, out, C, N, c.B, C, N * C, kRows);
-  if (c.gate) okm = okm && make_tmap_bf16_3d(&tg, c.gate, C, N, c.B, c.gate_stride, N * c.gate_stride, kRows);
-  else tg = tq;
+  CUtensorMap t[5];  // q, k, v, gate, out
+  bool okm = make_tmap_bf16_3d(&t[0], c.q, C, N, c.B, c.q_stride, N * c.q_stride, kRows) &&
+             make_tmap_bf16_3d(&t[1], c.k, Ck, Nk, c.B, c.k_stride, Nk * c.k_stride, kRows) &&
+             make_tmap_bf16_3d(&t[2], c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows) &&
+             make_tmap_bf16_3d(&t[4], out, C, N, c.B, C, N * C, kRows);
+  if (c.gate) okm = okm && make_tmap_bf16_3d(&t[3], c.gate, C, N, c.B, c.gate_stride, N * c.gate_stride, kRows);
+  else t[3] = t[0];
   if (!okm) return fail(SANA_ERR_CUDA, "windowed anchor: cuTensorMapEncodeTiled failed");
   once_per_context(kAttrWindowFwd, [] {
-    cudaFuncSetAttribute(window_fwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWinSmem);
-    cudaFuncSetAttribute(window_fwd_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWinSmem);
+    allow_smem<1, false>();
+    allow_smem<1, true>();
+    allow_smem<2, false>();
+    allow_smem<2, true>();
   });
   const WindowDev w{c.N, c.N_keys, c.N_keys - c.N, c.window, c.sinks, c.block, c.heads, c.kv_heads, c.lengths};
-  const dim3 grid((c.N + 2 * kRows - 1) / (2 * kRows), c.heads, c.B);
   const float sl = c.scale * 1.4426950408889634f;
-  int* sw = status_word();
-  if (c.gate)
-    window_fwd_kernel<true><<<grid, kThreads, kWinSmem, st>>>(tq, tk, tv, tg, ty, w, sl, lse, sw);
-  else
-    window_fwd_kernel<false><<<grid, kThreads, kWinSmem, st>>>(tq, tk, tv, tg, ty, w, sl, lse, sw);
+  // key tiles that a query tile sees at most
+  const long long all = (c.N_keys + kRows - 1) / kRows;
+  const long long reach = c.window ? ((long long)c.window + c.block + 2 * kRows - 3) / kRows + 1 +
+                                         (c.sinks + kRows - 1) / kRows
+                                   : all;
+  const bool single = (reach < all ? reach : all) <= kSingleReach;
+  if (single && c.gate) launch<1, true>(t, w, c.B, sl, lse, st);
+  else if (single) launch<1, false>(t, w, c.B, sl, lse, st);
+  else if (c.gate) launch<2, true>(t, w, c.B, sl, lse, st);
+  else launch<2, false>(t, w, c.B, sl, lse, st);
   return check_launch("window_fwd_kernel");
 }
 

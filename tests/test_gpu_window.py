@@ -122,6 +122,12 @@ CASES = [  # B, N, Nk, heads, kv, window, sinks, block, lengths, gated, packed
     (2, 300, 300, 2, 2, 80, 0, 40, [290, 33], True, True),
     (2, 1100, 1100, 6, 2, 256, 4, 1, [1100, 900], True, True),
     (1, 2300, 2300, 1, 1, 512, 16, 1, None, False, False),
+    (1, 2000, 2000, 8, 1, 64, 300, 1, None, False, True),          # three tiles of sinks, cut into shares
+    # more than ten key tiles to a query tile: two query tiles to a CTA
+    (1, 1700, 1700, 2, 1, 0, 0, 1, None, True, False),
+    (2, 1500, 1900, 4, 2, 1400, 9, 1, [1900, 1333], True, False),
+    (1, 1537, 1537, 2, 2, 1536, 100, 512, None, True, True),
+    (3, 1665, 1665, 2, 1, 1500, 40, 1, [1665, 130, 0], False, False),
 ]
 
 
