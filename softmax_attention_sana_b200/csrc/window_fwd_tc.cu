@@ -16,8 +16,8 @@
 //   producer warp : TMA Q_i once; K_u, V_u in rings of kQ stages over the key
 //                   tiles that any query tile sees (sinks, then the window); the
 //                   gate at the end, into the K ring
-//   MMA warp      : for each of them, where query tile i sees it: O_i += P_i V,
-//                   and S_i = Q_i K^T of the next one
+//   MMA warp      : for each of them, where query tile i sees it: S_i = Q_i K^T
+//                   of the next one, and O_i += P_i V
 //   kQ x 4 softmax warps (thread = query row): the score row in registers, masked
 //                   where some row of the query tile sees the key tile in part;
 //                   row max, lazy rescaling of O in TMEM (where a max passes the
@@ -26,7 +26,12 @@
 //                   1/l, gate, lse and the TMA store.
 // Registers: a softmax thread holds 128 scores, more than the 168 registers of
 // an even share, so the other warps give some of theirs up.
-// TMEM: S_i, then O_i, 128 columns each; P_i over the first half of S_i.
+// TMEM, two query tiles: one S buffer for both in turn (a warpgroup takes its
+// scores to registers at once, so the next product need not wait for its
+// exponentials), P_0, P_1 of 64 columns, O_0, O_1: 512 in all.  The tensor core
+// then always has a product to do: 16384 x 16 rows, no window: 3010 cycles a step
+// of both tiles with P over S, four products are 2048.  One query tile: S with P
+// over its first half, and O, 256 columns.
 //
 // Bound by the tensor core (4 * 128 flops per pair and head) with the MUFU unit
 // close behind: a quarter of the exponentials run as a cubic on the FMA pipe.
@@ -98,6 +103,7 @@ struct WinCtl {
   uint64_t k_full[kQ], k_empty[kQ];
   uint64_t v_full[kQ], v_empty[kQ];
   uint64_t s_full[kQ], p_full[kQ][2], pv_done[kQ];  // p_full[tile][half of the keys]
+  uint64_t s_taken;  // two tiles: the scores last made are in registers
   uint64_t ysync[kQ];
   uint32_t tmem;
   int abort_flag;
@@ -186,6 +192,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       mbar_init(&ctl.pv_done[i], 1);
       mbar_init(&ctl.ysync[i], 128);
     }
+    mbar_init(&ctl.s_taken, 128);
     ctl.abort_flag = 0;
     mbar_fence_init();
     if (span.n > 0) {  // the first loads run while the rest of the CTA sets up
@@ -206,6 +213,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
+  const uint32_t t_s = tmem, t_p = kQ == 2 ? tmem + 128 : tmem, t_o = tmem + kQ * 128;  // P_i 64, O_i 128 columns on
 
   if (warp >= F::kWarpProd) {
     warpgroup_regs_dec<F::kRegsOther>();
@@ -261,56 +269,59 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
             const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_ss_lead(lead, tmem + i * 128, desc_advance(a, o), desc_advance(bk, o), idesc, kk != 0);
+            umma_ss_lead(lead, t_s, desc_advance(a, o), desc_advance(bk, o), idesc, kk != 0);
           }
           umma_commit_lead(lead, &ctl.s_full[i]);
         };
         auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys, or what of them some row sees
           const int steps = span.s[i].width(span.tile(u), w.sinks) / 16 - half * 4;
           const uint64_t bv = desc_local(desc_advance(dv0, (u % kStages) * kTileB + half * 8192));
-          const uint32_t ap = tmem + i * 128 + half * 32;
+          const uint32_t ap = t_p + i * 64 + half * 32;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps)
-              umma_ts_lead(lead, tmem + (kQ + i) * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+              umma_ts_lead(lead, t_o + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
                            (done[i] | half | kk) != 0);
         };
-        bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
-        if (ok) {
+        int made = 0;  // S products issued
+        // S may be overwritten: it is in registers (two tiles), or the product that
+        // reads P from it has finished
+        auto s_free = [&](int i) {
+          if (kQ == 2) return made == 0 || mbar_wait(&ctl.s_taken, (made - 1) & 1, wc, 0x97);
+          return done[i] == 0 || mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97);
+        };
+        auto next_s = [&](int i, int u) {
+          if (!s_free(i)) return false;
           tc_fence_after();
-          for (int i = 0; i < kQ; ++i)
-            if (span.active(i, 0)) issue_s(i, 0);
-          umma_commit_lead(lead, &ctl.k_empty[0]);
-        }
+          issue_s(i, u);
+          ++made;
+          return true;
+        };
+        // O_i += P_i V, half by half as P_i comes (O_i has been rescaled if needed)
+        auto next_pv = [&](int i, int u) {
+          for (int half = 0; half < 2; ++half) {
+            if (!mbar_wait(&ctl.p_full[i][half], done[i] & 1, wc, 0x94)) return false;
+            tc_fence_after();
+            issue_pv(i, u, half);
+          }
+          umma_commit_lead(lead, &ctl.pv_done[i]);
+          ++done[i];
+          return true;
+        };
+        bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i)
+          if (ok && span.active(i, 0)) ok = next_s(i, 0);
+        if (ok) umma_commit_lead(lead, &ctl.k_empty[0]);
         for (int u = 0; ok && u < span.n; ++u) {
           const bool more = u + 1 < span.n;
           if (!mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x95)) break;
           if (more && !mbar_wait(&ctl.k_full[(u + 1) % kStages], ((u + 1) / kStages) & 1, wc, 0x96)) break;
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
-            if (span.active(i, u)) {
-              // P_i is in TMEM, half by half, and O_i has been rescaled if needed
-              for (int half = 0; half < 2; ++half) {
-                if (!mbar_wait(&ctl.p_full[i][half], done[i] & 1, wc, 0x94)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                issue_pv(i, u, half);
-              }
-              if (!ok) break;
-              umma_commit_lead(lead, &ctl.pv_done[i]);
-              ++done[i];
-            }
-            if (span.active(i, u + 1)) {
-              // S_i is overwritten once the product that reads P_i from it has finished
-              if (done[i] && !mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              issue_s(i, u + 1);
-            }
+            if (kQ == 2 && ok && span.active(i, u + 1)) ok = next_s(i, u + 1);
+            if (ok && span.active(i, u)) ok = next_pv(i, u);
+            if (kQ == 1 && ok && span.active(i, u + 1)) ok = next_s(i, u + 1);
           }
           if (!ok) break;
           umma_commit_lead(lead, &ctl.v_empty[u % kStages]);
@@ -324,7 +335,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     const int qi = kQ == 1 ? 0 : warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tmem_s = tmem + qi * 128, tmem_o = tmem + (kQ + qi) * 128;
+    const uint32_t tmem_s = t_s + lane_base, tmem_p = t_p + qi * 64 + lane_base, tmem_o = t_o + qi * 128 + lane_base;
     const int row = row0 + qi * kRows + r;
     const int pos = w.off + row;
     const bool row_live = row < w.N && pos < len;
@@ -352,10 +363,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       uint32_t sc[4][32];  // the whole row
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c < chunks) tmem_ld32(tmem_s + lane_base + c * 32, sc[c]);
+        if (c < chunks) tmem_ld32(tmem_s + c * 32, sc[c]);
       tmem_ld_wait();
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_tie(sc[c]);
+      if (kQ == 2) {
+        tc_fence_before();
+        mbar_arrive(&ctl.s_taken);
+      }
       auto chunk_max = [&](const uint32_t (&x)[32], float t) {  // two chains of 3-input max
         float t2 = __uint_as_float(x[0]);
 #pragma unroll
@@ -401,12 +416,12 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
-            tmem_ld16(tmem_o + lane_base + c * 16, o);
+            tmem_ld16(tmem_o + c * 16, o);
             tmem_ld_wait();
             tmem_tie(o);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-            tmem_st16(tmem_o + lane_base + c * 16, o);
+            tmem_st16(tmem_o + c * 16, o);
           }
         }
       }
@@ -431,6 +446,13 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
         }
         fence_proxy_async_smem();
       }
+      if (kQ == 2 && done >= 1) {  // P of the tile before has been read
+        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x90))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (c < chunks) {
@@ -450,9 +472,9 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
             rs2 = add2(rs2, pk2(p0, p1));
             pk[i / 2] = f2_to_bf2(p0, p1);
           }
-          // over S columns that are in registers; after each half of the keys the
+          // (one tile: over S columns that are in registers); after each half of the keys the
           // product with V may start on it
-          tmem_st16(tmem_s + lane_base + c * 16, pk);
+          tmem_st16(tmem_p + c * 16, pk);
         }
         if (c & 1) {
           tmem_st_wait();
@@ -482,7 +504,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
         if (any) {  // else nothing was accumulated for this tile
-          tmem_ld32(tmem_o + lane_base + c * 32, o);
+          tmem_ld32(tmem_o + c * 32, o);
           tmem_ld_wait();
         }
 #pragma unroll
