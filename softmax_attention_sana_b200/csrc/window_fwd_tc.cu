@@ -16,8 +16,9 @@
 //   producer warp : TMA Q_i once; K_u, V_u in rings of kQ stages over the key
 //                   tiles that any query tile sees (sinks, then the window); the
 //                   gate at the end, into the K ring
-//   MMA warp      : for each of them, where query tile i sees it: S_i = Q_i K^T
-//                   of the next one, and O_i += P_i V
+//   two MMA warps : for each of them, where query tile i sees it, one S_i = Q_i K^T,
+//                   the other O_i += P_i V (waits and issues of one warp alone took
+//                   longer than the products)
 //   kQ x 4 softmax warps (thread = query row): the score row in registers, masked
 //                   where some row of the query tile sees the key tile in part;
 //                   row max, lazy rescaling of O in TMEM (where a max passes the
@@ -48,13 +49,13 @@ constexpr int kD = 128;
 constexpr int kRows = kWinTile;
 constexpr int kHalf = kRows * 64 * 2;  // 16 KB: 64 columns of a tile
 constexpr int kTileB = 2 * kHalf;      // 32 KB
-// Shape of a CTA with kQ query tiles: 4 kQ softmax warps, producer, MMA, two idle
-// warps; kQ stages of K and V.  Registers a thread: the softmax warps take more
+// Shape of a CTA with kQ query tiles: 4 kQ softmax warps, producer, two MMA warps, an
+// idle one; kQ stages of K and V.  Registers a thread: the softmax warps take more
 // than an even share from the others (3 - kQ CTAs on an SM).
 template <int kQ>
 struct Form {
   static constexpr int kThreads = 128 * kQ + 128;
-  static constexpr int kWarpProd = 4 * kQ, kWarpMma = 4 * kQ + 1;
+  static constexpr int kWarpProd = 4 * kQ, kWarpS = 4 * kQ + 1, kWarpPv = 4 * kQ + 2;
   static constexpr int kStages = kQ;
   static constexpr int kLaunchRegs = kQ == 2 ? 168 : 128;
   static constexpr int kRegsSoftmax = kQ == 2 ? 216 : 208, kRegsOther = kQ == 2 ? 72 : 48;
@@ -68,8 +69,9 @@ constexpr float kRescaleLog2 = 16.f;
 // tiles) 177 against 190 us, 4096 (34 tiles) 486 against 477 us; 32 heads on 8 key
 // heads with a gate: 210 against 244, 411 against 419, 1027 against 991 us.
 constexpr int kSingleReach = 10;
-// Of every 8 pairs of exponentials, on the FMA pipe (none: 493 us at window 4096, one 486, two 477, three 478).
-constexpr int kEmuPairs = 2;
+// Of every 8 pairs of exponentials, on the FMA pipe.  Under the power cap, 32768 rows,
+// 32 heads, window 4096: none 2146 us, one 2130, two 2158 us.
+constexpr int kEmuPairs = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^(sl * s - m) for two scores on the FMA pipe, m an integer below 2^22 in
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       }
     }
   }
-  if (warp == F::kWarpMma) {
+  if (warp == F::kWarpS) {
     tmem_alloc(&ctl.tmem, F::kTmemCols);
     tmem_relinquish();
   }
@@ -252,80 +254,74 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
           if (ok && kGate) mbar_drain(&ctl.g_full, 0);
         }
       }
-    } else if (warp == F::kWarpMma) {
-      // ------------------------------------------------ MMA issuer
+    } else if (warp == F::kWarpS) {
+      // ------------------------------------------------ S products
       if (span.n > 0) {  // the whole warp, its elected lane issues
         const uint32_t lead = elect_lead();
         const uint32_t idesc_s = idesc_bf16_f32(128, 0, 0, 0);  // Q K^T, both K-major; N by the tile's width
-        const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
         const uint64_t dq0 = smem_desc_sw128(smem_u32(q_s), 16, 1024);
         const uint64_t dk0 = smem_desc_sw128(smem_u32(k_s), 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
-        int done[kQ] = {};  // P V products issued for each query tile
-        auto issue_s = [&](int i, int u) {
-          const uint32_t idesc = idesc_s | (uint32_t)(span.s[i].width(span.tile(u), w.sinks) >> 3) << 17;
-          const uint64_t a = desc_local(desc_advance(dq0, i * kTileB));
-          const uint64_t bk = desc_local(desc_advance(dk0, (u % kStages) * kTileB));
-#pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            umma_ss_lead(lead, t_s, desc_advance(a, o), desc_advance(bk, o), idesc, kk != 0);
-          }
-          umma_commit_lead(lead, &ctl.s_full[i]);
-        };
-        auto issue_pv = [&](int i, int u, int half) {  // over 64 of the keys, or what of them some row sees
-          const int steps = span.s[i].width(span.tile(u), w.sinks) / 16 - half * 4;
-          const uint64_t bv = desc_local(desc_advance(dv0, (u % kStages) * kTileB + half * 8192));
-          const uint32_t ap = t_p + i * 64 + half * 32;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (kk < steps)
-              umma_ts_lead(lead, t_o + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
-                           (done[i] | half | kk) != 0);
-        };
-        int made = 0;  // S products issued
-        // S may be overwritten: it is in registers (two tiles), or the product that
-        // reads P from it has finished
-        auto s_free = [&](int i) {
-          if (kQ == 2) return made == 0 || mbar_wait(&ctl.s_taken, (made - 1) & 1, wc, 0x97);
-          return done[i] == 0 || mbar_wait(&ctl.pv_done[i], (done[i] - 1) & 1, wc, 0x97);
-        };
-        auto next_s = [&](int i, int u) {
-          if (!s_free(i)) return false;
-          tc_fence_after();
-          issue_s(i, u);
-          ++made;
-          return true;
-        };
-        // O_i += P_i V, half by half as P_i comes (O_i has been rescaled if needed)
-        auto next_pv = [&](int i, int u) {
-          for (int half = 0; half < 2; ++half) {
-            if (!mbar_wait(&ctl.p_full[i][half], done[i] & 1, wc, 0x94)) return false;
-            tc_fence_after();
-            issue_pv(i, u, half);
-          }
-          umma_commit_lead(lead, &ctl.pv_done[i]);
-          ++done[i];
-          return true;
-        };
-        bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93) && mbar_wait(&ctl.k_full[0], 0, wc, 0x96);
-#pragma unroll
-        for (int i = 0; i < kQ; ++i)
-          if (ok && span.active(i, 0)) ok = next_s(i, 0);
-        if (ok) umma_commit_lead(lead, &ctl.k_empty[0]);
+        int made = 0, mine[kQ] = {};  // S products issued, in all and for each query tile
+        bool ok = mbar_wait(&ctl.q_full, 0, wc, 0x93);
         for (int u = 0; ok && u < span.n; ++u) {
-          const bool more = u + 1 < span.n;
-          if (!mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x95)) break;
-          if (more && !mbar_wait(&ctl.k_full[(u + 1) % kStages], ((u + 1) / kStages) & 1, wc, 0x96)) break;
+          if (!mbar_wait(&ctl.k_full[u % kStages], (u / kStages) & 1, wc, 0x96)) break;
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
-            if (kQ == 2 && ok && span.active(i, u + 1)) ok = next_s(i, u + 1);
-            if (ok && span.active(i, u)) ok = next_pv(i, u);
-            if (kQ == 1 && ok && span.active(i, u + 1)) ok = next_s(i, u + 1);
+            if (!ok || !span.active(i, u)) continue;
+            // S may be overwritten: it is in registers (two tiles), or the product
+            // that reads P from it has finished
+            if (kQ == 2) ok = made == 0 || mbar_wait(&ctl.s_taken, (made - 1) & 1, wc, 0x97);
+            else ok = mine[i] == 0 || mbar_wait(&ctl.pv_done[i], (mine[i] - 1) & 1, wc, 0x97);
+            if (!ok) continue;
+            tc_fence_after();
+            const uint32_t idesc = idesc_s | (uint32_t)(span.s[i].width(span.tile(u), w.sinks) >> 3) << 17;
+            const uint64_t a = desc_local(desc_advance(dq0, i * kTileB));
+            const uint64_t bk = desc_local(desc_advance(dk0, (u % kStages) * kTileB));
+#pragma unroll
+            for (int kk = 0; kk < kD / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+              umma_ss_lead(lead, t_s, desc_advance(a, o), desc_advance(bk, o), idesc, kk != 0);
+            }
+            umma_commit_lead(lead, &ctl.s_full[i]);
+            ++made;
+            ++mine[i];
           }
-          if (!ok) break;
-          umma_commit_lead(lead, &ctl.v_empty[u % kStages]);
-          if (more) umma_commit_lead(lead, &ctl.k_empty[(u + 1) % kStages]);
+          if (ok) umma_commit_lead(lead, &ctl.k_empty[u % kStages]);
+        }
+      }
+    } else if (warp == F::kWarpPv) {
+      // ------------------------------------------------ O += P V products
+      if (span.n > 0) {
+        const uint32_t lead = elect_lead();
+        const uint32_t idesc_o = idesc_bf16_f32(128, 128, 0, 1);  // P (TMEM) V, V MN-major
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(v_s), kHalf, 1024);
+        int done[kQ] = {};
+        bool ok = true;
+        for (int u = 0; ok && u < span.n; ++u) {
+          if (!mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x95)) break;
+#pragma unroll
+          for (int i = 0; i < kQ; ++i) {
+            if (!ok || !span.active(i, u)) continue;
+            const int steps = span.s[i].width(span.tile(u), w.sinks) / 16;
+            // half by half as P_i comes (O_i has been rescaled if needed)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait(&ctl.p_full[i][half], done[i] & 1, wc, 0x94);
+              if (!ok) continue;
+              tc_fence_after();
+              const uint64_t bv = desc_local(desc_advance(dv0, (u % kStages) * kTileB + half * 8192));
+              const uint32_t ap = t_p + i * 64 + half * 32;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (half * 4 + kk < steps)
+                  umma_ts_lead(lead, t_o + i * 128, ap + kk * 8, desc_advance(bv, kk * 2048), idesc_o,
+                               (done[i] | half | kk) != 0);
+            }
+            if (!ok) continue;
+            umma_commit_lead(lead, &ctl.pv_done[i]);
+            ++done[i];
+          }
+          if (ok) umma_commit_lead(lead, &ctl.v_empty[u % kStages]);
         }
       }
     }
@@ -371,14 +367,15 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
         tc_fence_before();
         mbar_arrive(&ctl.s_taken);
       }
-      auto chunk_max = [&](const uint32_t (&x)[32], float t) {  // two chains of 3-input max
-        float t2 = __uint_as_float(x[0]);
+      auto chunk_max = [&](const uint32_t (&x)[32]) {  // two chains of 3-input max
+        float t = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+        float t2 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
 #pragma unroll
-        for (int i = 1; i < 31; i += 4) {
+        for (int i = 6; i < 30; i += 4) {
           t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          if (i + 3 < 32) t2 = max3(t2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          t2 = max3(t2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
         }
-        return max3(t, t2, __uint_as_float(x[31]));
+        return fmaxf(max3(t, __uint_as_float(x[30]), __uint_as_float(x[31])), t2);
       };
       if (masked) {
 #pragma unroll
@@ -390,9 +387,13 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
         }
       }
       float top = -INFINITY;
+      if (chunks == 4) {
+        top = fmaxf(fmaxf(chunk_max(sc[0]), chunk_max(sc[1])), fmaxf(chunk_max(sc[2]), chunk_max(sc[3])));
+      } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < chunks) top = chunk_max(sc[c], top);
+        for (int c = 0; c < 3; ++c)
+          if (c < chunks) top = fmaxf(top, chunk_max(sc[c]));
+      }
       top *= sl;
       // The reference moves where the row's max passes it, on its first key or
       // by more than 2^16.  It is rounded up to an integer for the folded
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == F::kWarpMma) {
+  if (warp == F::kWarpS) {
     if (*wc.abort_flag) {  // MMAs in flight finish before TMEM is freed
       for (int i = 0; i < kQ; ++i) {
         const int n = span.s[i].count();
