@@ -1,5 +1,5 @@
-// Small device helpers of the softmax kernels: base-2 exponential, packed fp32
-// pairs, three-input maximum, shared-memory alignment.
+// Small device helpers of the windowed anchor and the query/key norm: base-2
+// exponential, packed fp32 pairs, three-input maximum, shared-memory alignment.
 #pragma once
 
 #include "sana_common.cuh"

@@ -39,6 +39,10 @@ constexpr int kUnrollBwd = sizeof(T) == 2 ? 4 : 2;
 template <class T>
 constexpr int kResident = sizeof(T) == 2 ? 7 : 4;
 
+__device__ __forceinline__ void report_bad_position(int* status) {
+  atomicCAS(status, 0, kDevBadPosition << 16);
+}
+
 // Eight consecutive elements of a row as loaded.
 template <class T>
 struct Vec8;

@@ -222,6 +222,9 @@ sana_status mx_gemm_run_parts(long long M, int N, int K, const void* xq, const v
                               long long ldo, int epilogue, cudaStream_t st);
 
 // ---------------------------------------------------------------- rotary positions, q/k norm
+// Device status (beside kDevTimeout): a token's position lies outside the rotary
+// table (the kernel reads the nearest row).
+constexpr int kDevBadPosition = 2;
 // How a kernel finds the angles of a token: a table of (cos, sin) by position
 // (table != nullptr; position = offset + n, or offset + positions[b][n]), or
 // the 3D tables of a video grid.

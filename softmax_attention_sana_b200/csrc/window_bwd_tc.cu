@@ -35,6 +35,7 @@
 
 #include "f32x2.cuh"
 #include "sana_internal.h"
+#include "tc_warp.cuh"
 #include "window.cuh"
 
 namespace sana {
