@@ -834,7 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&ctl.ds_full);
     }
     // ---------------- epilogue: each quarter writes its 32 columns
-    if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dq_done, (steps - 1) & 1, wc, 0xba));
+    // Nothing above waits for dQ(steps - 2): its phase is waited for first, or the
+    // parity of the last one would be taken for done while that one still runs.
+    // (dQ(steps - 3) ended before the last S was made.)
+    for (int t = max(steps - 2, 0); ok && t < steps; ++t)
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dq_done, t & 1, wc, 0xba));
     if (ok) {
       tc_fence_after();
       __nv_bfloat16* dst = dq + (((size_t)b * w.N + row) * w.heads + h) * kD + cg * 32;
@@ -861,7 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
-    if (*wc.abort_flag && steps > 0) mbar_drain(&ctl.dq_done, (steps - 1) & 1);
+    if (*wc.abort_flag)
+      for (int t = max(steps - 2, 0); t < steps; ++t) mbar_drain(&ctl.dq_done, t & 1);
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -17,13 +17,15 @@
 //   P^T = 2^(sl S^T - m) in bf16, turned to (row, key) order by movmatrix
 //   O^T (128 d x 8 rows) += V^T P^T     A = V^T by ldmatrix.trans
 // Running maximum and sum in fp32; the warps of a CTA and then the CTAs of a
-// (sequence, key head) are joined in a fixed order.  64 sequences of 8320 visible keys,
-// 16 query heads on 2 key heads: 93 us for 537 MB, 88% of the measured HBM rate; of
-// ragged lengths, 407 MB, 76 us (loads straight to registers, no ring: 93 us).
+// (sequence, key head) are joined in a fixed order: where they fit a cluster of up to
+// eight, in one another's shared memory, else through the workspace and a second kernel.  64 sequences of 8320 visible keys,
+// 16 query heads on 2 key heads: 88 us for 537 MB, 93% of the measured HBM rate; of
+// ragged lengths, 407 MB, 78 us (loads straight to registers, no ring: 93 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "f32x2.cuh"
+#include "pair.cuh"
 #include "pdl.cuh"
 #include "sana_internal.h"
 
@@ -38,6 +40,7 @@ constexpr int kBox = 16;                // rows of a TMA box
 constexpr int kStages = 3;
 constexpr int kHalf = kTile * 128;      // 64 columns of a tile's K or V, 8 KB
 constexpr int kStageB = 4 * kHalf;      // K and V of a tile, 32 KB
+constexpr int kCluster = 8;             // splits that are joined within a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeDev {
@@ -146,7 +149,14 @@ struct DecodeCtl {
 // Dynamic shared memory: the ring; when its last tile is used, the warps' sums.
 constexpr size_t kDecodeSmem = kStages * (size_t)kStageB + 1024;
 
-template <int NT>
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// kJoined: the splits of an item are one cluster.
+template <int NT, bool kJoined>
 __global__ void __launch_bounds__(kThreads, 2)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
@@ -154,14 +164,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   constexpr int kRowsT = 8 * NT;
   extern __shared__ uint8_t smem_raw[];
   __shared__ DecodeCtl ctl;
-  __shared__ float sm_m[kWarps][kRowsT], sm_l[kWarps][kRowsT];
+  __shared__ float sm_m[kWarps][kRowsT], sm_l[kWarps][kRowsT], sm_ml[kRowsT][2];
   uint8_t* ring = align1024(smem_raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, a = lane >> 2, c = lane & 3;
   const int splits = gridDim.x, split = blockIdx.x, b = blockIdx.z;
   const int hk = blockIdx.y / d.row_tiles, rt = blockIdx.y - hk * d.row_tiles;
   const int group = d.heads / d.kv_heads, rows = group * d.N, row0 = rt * kRowsT;
   const int len = __ldg(d.lengths + b);
-  griddep_launch_next();
+  if (!kJoined) griddep_launch_next();
 
   if (len < 0) {  // an empty batch entry
     if (split == 0)
@@ -223,6 +233,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();  // the ring has become the warps' sums
     __syncthreads();
+    if (kJoined) {
+      cluster_sync();
+      cluster_sync();
+    }
     return;
   }
 
@@ -376,6 +390,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (splits == 1) {
       write_out(d, b, hk, row0 + r, threadIdx.x, v, l);
+    } else if (kJoined) {
+      sm_o[0][r][threadIdx.x] = v;
+      if (threadIdx.x == 0) {
+        sm_ml[r][0] = top;
+        sm_ml[r][1] = l;
+      }
     } else {
       part[r * kD + threadIdx.x] = v;
       if (threadIdx.x == 0) {
@@ -383,6 +403,35 @@ __global__ void __launch_bounds__(kThreads, 2)
         part_ml[2 * r + 1] = l;
       }
     }
+  }
+  if (kJoined) {
+    cluster_sync();
+    // this CTA joins every splits-th row over the cluster
+    for (int r = split; r < kRowsT && row0 + r < rows; r += splits) {
+      float mk[kCluster], lk[kCluster], vk[kCluster];  // all on their way at once
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) {
+        mk[k] = -INFINITY;
+        lk[k] = vk[k] = 0.f;
+        if (k < splits) {
+          mk[k] = load_cluster(cluster_addr(&sm_ml[r][0], k));
+          lk[k] = load_cluster(cluster_addr(&sm_ml[r][1], k));
+          vk[k] = load_cluster(cluster_addr(&sm_o[0][r][threadIdx.x], k));
+        }
+      }
+      float top = mk[0], l = 0.f, v = 0.f;
+#pragma unroll
+      for (int k = 1; k < kCluster; ++k) top = fmaxf(top, mk[k]);
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int k = 0; k < kCluster; ++k) {
+        const float f = ex2(mk[k] - ref);
+        l = fmaf(f, lk[k], l);
+        v = fmaf(f, vk[k], v);
+      }
+      write_out(d, b, hk, row0 + r, threadIdx.x, v, l);
+    }
+    cluster_sync();  // nobody leaves while its sums are read
   }
 }
 
@@ -409,11 +458,15 @@ __global__ void __launch_bounds__(kD) window_decode_join_kernel(const DecodeDev 
 
 struct DecodePlan {
   int nt, row_tiles, splits;
+  bool joined;  // the splits of an item are a cluster
 };
 // Rows: one tile of 8 where they fit, else tiles of 16 (a second pass over the
 // keys costs more than the registers of 16 rows).  Splits: of those that the key
 // tiles allow, the one whose waves of CTAs (two fit on an SM) are soonest done,
-// with a CTA's start and end counted as two tiles.  64 sequences, 2 key heads,
+// with a CTA's start and end counted as two tiles and the second kernel as three.
+// Splits of one wave are clusters where they fit one (4 sequences of 1028 keys: 7.2
+// against 9.7 us; in several waves clusters wait for room: 91 against 79 us for 16
+// sequences, 24 key heads, 2052 keys).  64 sequences, 2 key heads,
 // 8320 keys: 2 splits in one wave 93 us, 4 in two 97 us, 9 in four 106 us; 16
 // sequences, 24 key heads, 2052 keys: 1 split in two waves 89 us, 3 in four 80 us.
 DecodePlan decode_plan(const DecodeCall& c) {
@@ -429,10 +482,12 @@ DecodePlan decode_plan(const DecodeCall& c) {
   most = most < 1 ? 1 : most > tiles ? tiles : most;
   long long best = 0;
   for (long long s = 1; s <= most; ++s) {
-    const long long cost = (items * s + slots - 1) / slots * ((tiles + s - 1) / s + 2);
+    const bool joined = s <= kCluster && items * s <= slots;
+    const long long cost = (items * s + slots - 1) / slots * ((tiles + s - 1) / s + 2) + (joined ? 0 : 3);
     if (best == 0 || cost < best) {
       best = cost;
       p.splits = (int)s;
+      p.joined = joined && s > 1;
     }
   }
   return p;
@@ -442,7 +497,7 @@ DecodePlan decode_plan(const DecodeCall& c) {
 
 size_t window_decode_ws_bytes(const DecodeCall& c) {
   const DecodePlan p = decode_plan(c);
-  if (p.splits == 1) return 0;
+  if (p.splits == 1 || p.joined) return 0;
   return align_up((size_t)c.B * c.kv_heads * p.row_tiles * p.splits * 8 * p.nt * (kD + 2) * sizeof(float), 256);
 }
 
@@ -462,13 +517,32 @@ sana_status window_decode_run(const DecodeCall& c, const void* q, const void* k_
       !make_tmap_bf16_3d(&tvn, v_new, C, N, c.B, C, N * C, kBox))
     return fail(SANA_ERR_CUDA, "windowed anchor step: cuTensorMapEncodeTiled failed");
   once_per_context(kAttrWindowDecode, [] {
-    cudaFuncSetAttribute(window_decode_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
-    cudaFuncSetAttribute(window_decode_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+    cudaFuncSetAttribute(window_decode_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+    cudaFuncSetAttribute(window_decode_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+    cudaFuncSetAttribute(window_decode_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
+    cudaFuncSetAttribute(window_decode_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kDecodeSmem);
   });
   int* sw = status_word();
   const dim3 grid(p.splits, c.kv_heads * p.row_tiles, c.B);
-  if (p.nt == 1) window_decode_kernel<1><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
-  else window_decode_kernel<2><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
+  if (p.joined) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kDecodeSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.nt == 1) cudaLaunchKernelEx(&cfg, window_decode_kernel<1, true>, tk, tv, tkn, tvn, d, sw);
+    else cudaLaunchKernelEx(&cfg, window_decode_kernel<2, true>, tk, tv, tkn, tvn, d, sw);
+    return check_launch("window_decode_kernel");
+  }
+  if (p.nt == 1) window_decode_kernel<1, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
+  else window_decode_kernel<2, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
   if (sana_status e = check_launch("window_decode_kernel")) return e;
   if (p.splits > 1) {
     launch_dependent(window_decode_join_kernel, dim3(c.heads / c.kv_heads * c.N, c.kv_heads, c.B), dim3(kD), 0, st,

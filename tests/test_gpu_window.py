@@ -154,6 +154,25 @@ def test_forward_and_backward_match_the_dense_formulas(case):
     sana.sync_status()
 
 
+@pytest.mark.parametrize("N,heads,kv,window,block,lengths", [(1232, 16, 4, 561, 242, None), (700, 8, 8, 300, 1, [700, 433]),
+                                                           (2500, 4, 1, 0, 1, None), (900, 16, 2, 128, 1, None)])
+def test_many_runs_give_the_same_bits(N, heads, kv, window, block, lengths):
+    """Every sum has its order: 40 forward and backward runs, with work on the GPU before and after
+    each, agree bit by bit (a product read before it is whole shows here)."""
+    B = 1 if lengths is None else len(lengths)
+    q, k, v, gate, dy = inputs(9, B, N, N, heads, kv, True, False, lengths)
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    kw = dict(window=window, sinks=3, block=block, lengths=lt)
+    first = None
+    for _ in range(40):
+        y, lse = sana.window_anchor_fwd(q, k, v, gate, heads, kv, want_lse=True, **kw)
+        run = (y, lse) + sana.window_anchor_bwd(q, k, v, gate, y, lse, dy, heads, kv, **kw)
+        if first is None:
+            first = run
+        assert all(torch.equal(a, b) for a, b in zip(run, first))
+    sana.sync_status()
+
+
 def test_gradients_agree_with_differences():
     """Along random directions, the 64-bit forward's central differences match the gradients to the
     gradients' own error (2 % of the directional derivative's scale: 2^-8 roundings of some hundred
