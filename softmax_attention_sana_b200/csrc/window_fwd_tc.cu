@@ -349,7 +349,15 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     float m = -INFINITY, l = 0.f;  // row max reference and sum, base 2
     bool ok = true;
     int done = 0;
+    const bool pads = len < w.N_keys;  // V may hold padding rows, to be zeroed below
     for (int u = 0; ok && u < span.n; ++u) {
+      // Every V in turn, so that the parity waited for is always the next one.  (One
+      // query tile: S(u) was made after P V(u - 1), so V(u) is the next one anyway,
+      // and is waited for only where it is touched.)
+      if (kQ == 2 && pads && !__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
+        ok = false;
+        break;
+      }
       if (!span.active(qi, u)) continue;
       const int key0 = span.tile(u) * kRows;
       const int chunks = span.s[qi].width(span.tile(u), w.sinks) / 32;  // of 32 columns
@@ -434,11 +442,10 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       const uint64_t cfold = pk2(12582912.f - m_use, 12582912.f - m_use);
       const float s_lo = (m_use - 126.f) * inv_sl;
       uint64_t rs2 = pk2(0.f, 0.f);
-      const bool tail = key0 + kRows > len && len < w.N_keys;
-      if (tail) {
+      if (pads && key0 + kRows > len) {
         // padding rows of V meet P = 0: zero them, whatever they hold (both
         // warpgroups write the same zeros before their own product reads V)
-        if (!__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
+        if (kQ == 1 && !__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
           ok = false;
           break;
         }
