@@ -20,7 +20,7 @@
 // a row sits in head_dim / 8 neighbouring lanes (the partner in the half layout
 // is a shuffle away), several row groups in flight.  480p grid (32760 tokens, 16 + 16
 // heads of 128, bf16): 87 us for 537 MB, 94% of the measured HBM rate; gradient of
-// 2 x 4001 tokens, 32 + 8 heads: 55 us for 246 MB (two tensors to load: 68%).  Bulk
+// 2 x 4001 tokens, 32 + 8 heads: 51 us for 246 MB (two tensors to load: 73%).  Bulk
 // copies into a ring in shared memory instead of loads to registers: 126 us.
 #include "f32x2.cuh"
 #include "pdl.cuh"
@@ -314,84 +314,100 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<T>)
   }
 }
 
-// Gradient.  A warp takes whole tokens (token index = warp, warp + all warps,
-// ...), its query heads and then its key heads, and adds the weights' gradient
-// in registers over all of them; the CTA's warps are then added in warp order
-// and the CTA's sums written out, to be added in CTA order by the next kernel:
-// the summation order depends on the shape alone.
+// Gradient.  The work is a row of steps, per token those of its query heads
+// (kUnrollBwd row groups each) and then those of its key heads; every warp takes
+// an equal run of them (whole tokens to a warp left the last round a third empty:
+// 2 x 4001 tokens 56 against 51 us) and adds the weights' gradient in registers
+// over its run; the CTA's warps are then added in warp order and the CTA's sums
+// written out, to be added in CTA order by the next kernel: the summation order
+// depends on the shape alone.
 template <class T, int LPR, bool HALF>
 __global__ void __launch_bounds__(32 * kWarpsBwd, 2)
     qk_norm_rope_bwd_kernel(const QkTensors a, const RotaryDev rt, float eps, float q_mul,
                             float* __restrict__ dw_part, int* status) {
-  constexpr int D = LPR * 8, RPW = 32 / LPR;
+  constexpr int D = LPR * 8, RPW = 32 / LPR, kU = kUnrollBwd<T>;
   __shared__ float red[kWarpsBwd][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = (lane % LPR) * 8, sub_row = lane / LPR;
   Turn<LPR, HALF> turn;
   turn.init(rt, lane);
   uint64_t dw[2][4] = {};
-  const long long tokens = (long long)a.B * a.N;
-  for (long long token = (long long)blockIdx.x * kWarpsBwd + warp; token < tokens;
-       token += (long long)gridDim.x * kWarpsBwd) {
-    const int b = (int)((unsigned)token / (unsigned)a.N), n = (int)token - b * a.N;
-    turn.fetch(rt, b, n, lane, status);
+  const int steps_q = (a.heads + kU * RPW - 1) / (kU * RPW), steps_k = (a.kv_heads + kU * RPW - 1) / (kU * RPW);
+  const int per_token = steps_q + steps_k;
+  const long long all = (long long)a.B * a.N * per_token, warps = (long long)gridDim.x * kWarpsBwd;
+  const long long me = (long long)blockIdx.x * kWarpsBwd + warp;
+  long long left = all * (me + 1) / warps - all * me / warps;
+  long long token = all * me / warps / per_token;
+  int step = (int)(all * me / warps - token * per_token);
+  bool fresh = true;  // the token's angles have to be looked up
+  for (; left > 0; --left) {
+    const bool is_q = step < steps_q;
+    const int heads = is_q ? a.heads : a.kv_heads;
+    const int h = (is_q ? step : step - steps_q) * kU * RPW;
+    const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride) + col;
+    const T* dy = static_cast<const T*>(is_q ? a.dq_out : a.dk_out) + (size_t)token * heads * D + col;
+    T* dx = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D + col;
+    Vec8<T> rx[kU], rg[kU];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const bool is_q = side == 0;
-      const int heads = is_q ? a.heads : a.kv_heads;
-      const T* x = static_cast<const T*>(is_q ? a.q : a.k) + (size_t)token * (is_q ? a.q_stride : a.k_stride) + col;
-      const T* dy = static_cast<const T*>(is_q ? a.dq_out : a.dk_out) + (size_t)token * heads * D + col;
-      T* dx = static_cast<T*>(is_q ? a.q_out : a.k_out) + (size_t)token * heads * D + col;
-      const float m = is_q ? q_mul : 1.f;
-      uint64_t ca[4], cb[4], w[4];
+    for (int u = 0; u < kU; ++u) {
+      const int hr = h + u * RPW + sub_row;
+      if (hr < heads) {
+        rx[u].load(x + (size_t)hr * D);
+        rg[u].load(dy + (size_t)hr * D);
+      } else {
+        rx[u].zero();
+        rg[u].zero();
+      }
+    }
+    if (fresh) {
+      const int b = (int)((unsigned)token / (unsigned)a.N);
+      turn.fetch(rt, b, (int)token - b * a.N, lane, status);
+    }
+    const float m = is_q ? q_mul : 1.f;
+    uint64_t ca[4], cb[4], w[4], sum[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ca[i] = pk2(m * turn.own(2 * i), m * turn.own(2 * i + 1));
+      cb[i] = pk2(m * turn.other(2 * i, true), m * turn.other(2 * i + 1, true));
+    }
+    load_w(is_q ? a.wq : a.wk, col, w);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (h + u * RPW >= heads) break;  // warp-uniform
+      const int hr = h + u * RPW + sub_row;
+      uint64_t f[4], d[4], g[4];
+      rx[u].get(f);
+      rg[u].get(d);
+      turn.apply(rg[u], d, ca, cb, g);
+      float ss = sum_squares(f), dot, t1;
+      uint64_t gf = 0, gw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ca[i] = pk2(m * turn.own(2 * i), m * turn.own(2 * i + 1));
-        cb[i] = pk2(m * turn.other(2 * i, true), m * turn.other(2 * i + 1, true));
+        gw[i] = mul2(g[i], w[i]);
+        gf = fma2(gw[i], f[i], gf);
       }
-      load_w(is_q ? a.wq : a.wk, col, w);
-      for (int h = 0; h < heads; h += kUnrollBwd<T> * RPW) {
-        Vec8<T> rx[kUnrollBwd<T>], rg[kUnrollBwd<T>];
+      up2(gf, dot, t1);
+      dot += t1;
+      row_sum2<LPR>(ss, dot, lane);
+      const float r = rsqrtf(ss * (1.f / D) + eps);
+      const float k3 = -r * r * r * (dot * (1.f / D));
+      const uint64_t r2 = pk2(r, r), k32 = pk2(k3, k3);
 #pragma unroll
-        for (int u = 0; u < kUnrollBwd<T>; ++u) {
-          const int hr = h + u * RPW + sub_row;
-          if (hr < heads) {
-            rx[u].load(x + (size_t)hr * D);
-            rg[u].load(dy + (size_t)hr * D);
-          } else {
-            rx[u].zero();
-            rg[u].zero();
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kUnrollBwd<T>; ++u) {
-          if (h + u * RPW >= heads) break;  // warp-uniform
-          const int hr = h + u * RPW + sub_row;
-          uint64_t f[4], d[4], g[4];
-          rx[u].get(f);
-          rg[u].get(d);
-          turn.apply(rg[u], d, ca, cb, g);
-          float ss = sum_squares(f), dot, t1;
-          uint64_t gf = 0, gw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            gw[i] = mul2(g[i], w[i]);
-            gf = fma2(gw[i], f[i], gf);
-          }
-          up2(gf, dot, t1);
-          dot += t1;
-          row_sum2<LPR>(ss, dot, lane);
-          const float r = rsqrtf(ss * (1.f / D) + eps);
-          const float k3 = -r * r * r * (dot * (1.f / D));
-          const uint64_t r2 = pk2(r, r), k32 = pk2(k3, k3);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dw[side][i] = fma2(g[i], mul2(f[i], r2), dw[side][i]);
-            g[i] = fma2(k32, f[i], mul2(r2, gw[i]));
-          }
-          if (hr < heads) Vec8<T>::store(dx + (size_t)hr * D, g);
-        }
+      for (int i = 0; i < 4; ++i) {
+        sum[i] = fma2(g[i], mul2(f[i], r2), sum[i]);
+        g[i] = fma2(k32, f[i], mul2(r2, gw[i]));
       }
+      if (hr < heads) Vec8<T>::store(dx + (size_t)hr * D, g);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (is_q) dw[0][i] = add2(dw[0][i], sum[i]);
+      else dw[1][i] = add2(dw[1][i], sum[i]);
+    }
+    fresh = ++step == per_token;
+    if (fresh) {
+      step = 0;
+      ++token;
     }
   }
   // rows of the warp, then warps of the CTA, in a fixed order
