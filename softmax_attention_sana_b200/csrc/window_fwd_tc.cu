@@ -8,11 +8,11 @@
 // to bf16 as the A operand of P V: each rounding is 2^-9 of its term and they
 // average out).
 //
-// One CTA per (batch, query head, kQ 128-query tiles).  With two query tiles they
-// share the K and V tiles in shared memory and their softmax warpgroups alternate
-// with the tensor core; with one, two CTAs share an SM, alternate the same way,
-// and one's start and end run under the other's loop, at twice the K and V
-// traffic: the form for short windows.
+// One CTA per (batch, kQ 128-query tiles: of one query head, or of two that share a
+// key head).  With two query tiles they share the K and V tiles in shared memory
+// and their softmax warpgroups alternate with the tensor core; with one, two CTAs
+// share an SM, alternate the same way, and one's start and end run under the
+// other's loop, at twice the K and V traffic: the form for short windows.
 //   producer warp : TMA Q_i once; K_u, V_u in rings of kQ stages over the key
 //                   tiles that any query tile sees (sinks, then the window); the
 //                   gate at the end, into the K ring
@@ -123,14 +123,14 @@ struct CtaSpan {
   __device__ __forceinline__ bool active(int i, int u) const { return u < n && s[i].has(tile(u)); }
 };
 template <int kQ>
-__device__ __forceinline__ CtaSpan<kQ> cta_span(const WindowDev& w, int row0, int len) {
+__device__ __forceinline__ CtaSpan<kQ> cta_span(const WindowDev& w, int row0, int row_step, int len) {
   CtaSpan<kQ> p;
   int last = -1;
   p.w0 = 0x7fffffff;
   p.ns = 0;
 #pragma unroll
   for (int i = 0; i < kQ; ++i) {
-    const int a = row0 + i * kRows, b = min(a + kRows, w.N) - 1;
+    const int a = row0 + i * row_step, b = min(a + kRows, w.N) - 1;
     p.s[i] = window_span(w, w.off + a, w.off + b, len);
     if (p.s[i].w1 >= p.s[i].w0) {
       p.w0 = min(p.w0, p.s[i].w0);
@@ -147,7 +147,7 @@ template <int kQ, bool kGate>
 __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
-                      const __grid_constant__ CUtensorMap tm_y, const WindowDev w, float sl,
+                      const __grid_constant__ CUtensorMap tm_y, const WindowDev w, int by_head, float sl,
                       float* __restrict__ lse, int* status) {
   using F = Form<kQ>;
   constexpr int kStages = F::kStages;
@@ -160,11 +160,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the last query tiles see the most keys where the window is open: they start first
-  const int qp = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int hk = h / (w.heads / w.kv_heads);
-  const int row0 = qp * kQ * kRows;
+  const int qp = gridDim.x - 1 - blockIdx.x, b = blockIdx.z;
+  // query tile i: head h0 + i * head_step, rows from row0 + i * row_step on
+  const int head_step = kQ == 2 && by_head, row_step = head_step ? 0 : kRows;
+  const int h0 = blockIdx.y * (1 + head_step);
+  const int hk = h0 / (w.heads / w.kv_heads);
+  const int row0 = qp * (head_step ? kRows : kQ * kRows);
   const int len = window_length(w, b);
-  const CtaSpan<kQ> span = cta_span<kQ>(w, row0, len);
+  const CtaSpan<kQ> span = cta_span<kQ>(w, row0, row_step, len);
   const WaitCtx wc{&ctl.abort_flag, status};
 
   auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     if (span.n > 0) {  // the first loads run while the rest of the CTA sets up
       mbar_arrive_expect_tx(&ctl.q_full, kQ * kTileB);
       for (int i = 0; i < kQ; ++i)  // a tile past N reads as zeros
-        load_tile(q_s + i * kTileB, &tm_q, &ctl.q_full, h, row0 + i * kRows);
+        load_tile(q_s + i * kTileB, &tm_q, &ctl.q_full, h0 + i * head_step, row0 + i * row_step);
       for (int u = 0; u < min(span.n, kStages); ++u) {
         load_k(u);
         load_v(u);
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
             ok = mbar_wait(&ctl.k_empty[u % kStages], (u / kStages) & 1, wc, 0x9c);
           if (ok) {
             mbar_arrive_expect_tx(&ctl.g_full, kQ * kTileB);
-            for (int i = 0; i < kQ; ++i) load_tile(k_s + i * kTileB, &tm_g, &ctl.g_full, h, row0 + i * kRows);
+            for (int i = 0; i < kQ; ++i) load_tile(k_s + i * kTileB, &tm_g, &ctl.g_full, h0 + i * head_step, row0 + i * row_step);
           }
         }
         if (*wc.abort_flag) {  // loads still in flight land before the CTA exits
@@ -335,12 +338,12 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tmem_s = t_s + lane_base, tmem_p = t_p + qi * 64 + lane_base, tmem_o = t_o + qi * 128 + lane_base;
-    const int row = row0 + qi * kRows + r;
+    const int h = h0 + qi * head_step, tile0 = row0 + qi * row_step, row = tile0 + r;
     const int pos = w.off + row;
     const bool row_live = row < w.N && pos < len;
     // this row's limits, and those of the tile's first and last live rows
     const int end = min(window_end(w, pos), len), low = window_low(w, window_end(w, pos));
-    const int pos0 = w.off + row0 + qi * kRows;
+    const int pos0 = w.off + tile0;
     const int pos1 = min(min(pos0 + kRows, w.off + w.N), len) - 1;
     const int all_end = min(window_end(w, pos0), len);       // every live row sees below it
     const int all_low = window_low(w, window_end(w, max(pos1, 0)));  // every live row sees from it on
@@ -548,9 +551,9 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     }
     mbar_arrive(&ctl.ysync[qi]);
     ok = mbar_wait(&ctl.ysync[qi], 0, wc, 0x9b) && ok;
-    if (ok && r == 0 && row0 + qi * kRows < w.N) {  // a tile past N has nothing to store
-      tma_store_3d(&tm_y, ybuf, h * kD, row0 + qi * kRows, b);
-      tma_store_3d(&tm_y, ybuf + kHalf, h * kD + 64, row0 + qi * kRows, b);
+    if (ok && r == 0 && tile0 < w.N) {  // a tile past N has nothing to store
+      tma_store_3d(&tm_y, ybuf, h * kD, tile0, b);
+      tma_store_3d(&tm_y, ybuf + kHalf, h * kD + 64, tile0, b);
       bulk_commit();
       bulk_wait_read0();  // the staging may go; the grid's end makes the rows visible
     }
@@ -571,9 +574,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
 
 template <int kQ, bool kGate>
 void launch(const CUtensorMap* t, const WindowDev& w, int B, float sl, float* lse, cudaStream_t st) {
-  const dim3 grid((w.N + kQ * kRows - 1) / (kQ * kRows), w.heads, B);
-  window_fwd_kernel<kQ, kGate><<<grid, Form<kQ>::kThreads, Form<kQ>::kSmem, st>>>(t[0], t[1], t[2], t[3], t[4], w, sl,
-                                                                                lse, status_word());
+  // Two query heads of one key head make the better pair: both tiles see the same
+  // keys (two tiles of rows leave each other idle at one end of the window: 16384
+  // rows, 32 heads on 8, window 2048, 617 against 575 us).
+  const int by_head = kQ == 2 && w.heads / w.kv_heads % 2 == 0;
+  const int rows = by_head ? kRows : kQ * kRows;
+  const dim3 grid((w.N + rows - 1) / rows, by_head ? w.heads / 2 : w.heads, B);
+  window_fwd_kernel<kQ, kGate><<<grid, Form<kQ>::kThreads, Form<kQ>::kSmem, st>>>(t[0], t[1], t[2], t[3], t[4], w,
+                                                                                by_head, sl, lse, status_word());
 }
 template <int kQ, bool kGate>
 void allow_smem() {

@@ -128,6 +128,7 @@ CASES = [  # B, N, Nk, heads, kv, window, sinks, block, lengths, gated, packed
     (2, 1500, 1900, 4, 2, 1400, 9, 1, [1900, 1333], True, False),
     (1, 1537, 1537, 2, 2, 1536, 100, 512, None, True, True),
     (3, 1665, 1665, 2, 1, 1500, 40, 1, [1665, 130, 0], False, False),
+    (2, 1600, 1600, 3, 1, 0, 0, 1, [1600, 700], True, True),       # an odd group: pairs of rows
 ]
 
 
