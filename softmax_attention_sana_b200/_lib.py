@@ -626,11 +626,11 @@ def _norm_weight(w, name, q, D):
 
 def _out_like(out, name, q, width):
     """A contiguous (B, N, width) tensor like q: `out`, checked, or a new one."""
-    B, N, C = q.shape
     if out is None:
-        if C == width and q.is_contiguous():
+        if q.is_contiguous() and q.shape[2] == width:
             return torch.empty_like(q)
-        return q.new_empty((B, N, width))
+        return q.new_empty((*q.shape[:2], width))
+    B, N, _ = q.shape
     _need(out, name)
     if out.dtype is not q.dtype or out.shape != (B, N, width):
         raise ValueError(f"{name} must be {q.dtype} {(B, N, width)}")
@@ -645,7 +645,7 @@ def rotary_apply(q, k, rotary, heads, kv_heads, positions=None, offset=0, grid=N
     gradient).  k is None with kv_heads 0 (then k_out is None).  bf16 or fp32."""
     s, at = _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid)
     q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
-    k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
+    k_out = None if k is None else _out_like(k_out, "k_out", k, kv_heads * s.head_dim)
     _call_on(q, lib.sana_rotary_apply, s, _dtype_code(q), at, int(bool(inverse)), q.data_ptr(),
              _addr(k), q_mul, q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
@@ -659,7 +659,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, rotary, heads, kv_heads, positions=No
     _norm_weight(q_weight, "q_weight", q, s.head_dim)
     _norm_weight(k_weight, "k_weight", q, s.head_dim)
     q_out = _out_like(q_out, "q_out", q, heads * s.head_dim)
-    k_out = None if k is None else _out_like(k_out, "k_out", q, kv_heads * s.head_dim)
+    k_out = None if k is None else _out_like(k_out, "k_out", k, kv_heads * s.head_dim)
     _call_on(q, lib.sana_qk_norm_rope, s, _dtype_code(q), at, q.data_ptr(), _addr(k),
              _addr(q_weight), _addr(k_weight), eps, q_mul, q_out.data_ptr(), _addr(k_out))
     return q_out, k_out
@@ -681,9 +681,9 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, rotary, heads, kv
     dq_out = _out_like(dq_out, "dq_out", q, heads * D)
     if (dk_out is None) != (k is None):
         raise ValueError("dk_out goes with k")
-    dk_out = None if k is None else _out_like(dk_out, "dk_out", q, kv_heads * D)
+    dk_out = None if k is None else _out_like(dk_out, "dk_out", k, kv_heads * D)
     dq = _out_like(None, "dq", q, heads * D)
-    dk = None if k is None else _out_like(None, "dk", q, kv_heads * D)
+    dk = None if k is None else _out_like(None, "dk", k, kv_heads * D)
     dwq = torch.empty(D, dtype=torch.float32, device=q.device)
     dwk = None if k is None else torch.empty_like(dwq)
     if ws is None:
@@ -808,10 +808,11 @@ def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_hea
     s = WindowDecodeShape(B, N, heads, kv_heads, D, capacity, window, sinks, scale)
     out = _out_like(out, "out", q, C)
     if ws is None:
-        ws = _ws(lib.sana_window_anchor_decode_workspace_size(s), q.device)
+        need = lib.sana_window_anchor_decode_workspace_size(s)
+        ws = _ws(need, q.device) if need else None  # most steps of small batches need none
     _call_on(q, lib.sana_window_anchor_decode, s, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              _addr(gate), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
-             out.data_ptr(), *_ws_args(ws, q))
+             out.data_ptr(), *((None, 0) if ws is None else _ws_args(ws, q)))
     return out
 
 
