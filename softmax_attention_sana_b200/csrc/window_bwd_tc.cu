@@ -7,15 +7,16 @@
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i,
 // dk and dv summed over the query heads that share the key head.
 //
-// Four kernels; every sum runs in an order that the shape alone fixes:
+// Three kernels, each started while the one before it ends; every sum runs in an
+// order that the shape alone fixes:
 //   prep   row statistics (-lse log2 e, -delta), and with a gate do and dg (HBM)
-//   dkv    one CTA per (key tile, key head, batch, share of its query tiles):
-//          scores transposed (thread = key), S^T = K Q^T and dP^T = V dO^T, then
-//          dV += P^T dO and dK += dS^T Q with P^T and dS^T from TMEM
+//   grad   dkv blocks, one CTA per (key tile, key head, batch, share of its query
+//          tiles): scores transposed (thread = key), S^T = K Q^T and dP^T = V dO^T,
+//          then dV += P^T dO and dK += dS^T Q with P^T and dS^T from TMEM;
+//          dq blocks, one CTA per (query tile, query head, batch): S and dP once
+//          more, then dQ += dS K
 //   join   sums the shares of key tiles that were split (few key tiles, or the
-//          sinks, which every later query sees)
-//   dq     one CTA per (query tile, query head, batch): S and dP once more, then
-//          dQ += dS K.
+//          sinks, which every later query sees).
 // Making S and dP twice costs 7 products instead of 5, and keeps dQ out of
 // memory until it is whole: the other way round it would be added up in fp32
 // over the key tiles, 64 KB through L2 for every tile pair, in an order to be
@@ -31,13 +32,16 @@
 //   dq     tensor: dP(t+1) | dQ(t) | S(t+2)             warps: dS(t) | P(t+1)
 //          (two S buffers; dS over the S columns of its tile)
 // A product that overwrites what another reads waits for it by its barrier.
-// 16384 rows, 16 heads on 4 key heads, window 2048, 16 sinks: dkv 480 us, dq 350 us
-// (1.08 and 1.11 PFLOP/s), tensor pipe about 70% busy; in a long run the power cap
-// holds both.  One warp issues all products: with a second one for the dP chain dkv
-// took 542 us (the products then come in a worse order).
+// 16384 rows, 16 heads on 4 key heads, window 2048, 16 sinks: 815 us in all, 861 us
+// with dkv and dq as launches of their own (480 and 350 us: the dq blocks fill the
+// SMs that the last dkv wave leaves); 2 x 1023 rows, 8 heads, window 256: 40 against
+// 49 us.  Tensor pipe about 70% busy; in a long run the power cap holds it.  One warp
+// issues all products: with a second one for the dP chain dkv took 542 us (the
+// products then come in a worse order).
 #include <cuda.h>
 
 #include "f32x2.cuh"
+#include "pdl.cuh"
 #include "sana_internal.h"
 #include "tc_warp.cuh"
 #include "window.cuh"
@@ -103,6 +107,7 @@ __global__ void __launch_bounds__(256)
                        const float* __restrict__ lse, const WindowDev w, int n_pad,
                        float* __restrict__ nlse, float* __restrict__ ndelta,
                        __nv_bfloat16* __restrict__ d_o, __nv_bfloat16* __restrict__ dg) {
+  griddep_launch_next();
   const int sub = threadIdx.x & 15, hw = threadIdx.x >> 4;
   const int h = blockIdx.x % w.heads, b = blockIdx.z;
   const int len = window_length(w, b);
@@ -202,14 +207,15 @@ struct DkvCtl {
 // bytes from the 1024-aligned start), row statistics of each do stage.
 constexpr size_t kDkvSmem = (2 + kDeep + kShort) * (size_t)kTileB + kShort * 2 * kRows * sizeof(float);
 
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const WindowDev w, const DkvPlan plan, float sl, float scale, int n_pad,
-                      const float* __restrict__ nlse, const float* __restrict__ ndelta,
-                      float* __restrict__ part, __nv_bfloat16* __restrict__ dk,
-                      __nv_bfloat16* __restrict__ dv, int* status) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+// Block (x, hk, b) of `items` x kv_heads x B.
+__device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int items, int hk, int b,
+                                          const CUtensorMap& tm_q, const CUtensorMap& tm_do,
+                                          const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          const WindowDev& w, const DkvPlan& plan, float sl,
+                                          float scale, int n_pad, const float* __restrict__ nlse,
+                                          const float* __restrict__ ndelta, float* __restrict__ part,
+                                          __nv_bfloat16* __restrict__ dk,
+                                          __nv_bfloat16* __restrict__ dv, int* status) {
   uint8_t* k_s = smem;
   uint8_t* v_s = k_s + kTileB;
   uint8_t* q_s = v_s + kTileB;
@@ -218,10 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   DkvCtl& ctl = *reinterpret_cast<DkvCtl*>(stat + kShort * 2 * kRows);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.y, b = blockIdx.z, group = w.heads / w.kv_heads;
+  const int group = w.heads / w.kv_heads;
   int kt, share, parts;
   {
-    const int x = blockIdx.x, in_sinks = plan.sink_tiles * plan.sink_parts;
+    const int in_sinks = plan.sink_tiles * plan.sink_parts;
     if (x < in_sinks) {
       parts = plan.sink_parts;
       kt = x / parts;
@@ -282,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_tile(k_s, &tm_k, &ctl.kv_full, hk, kt * kRows);
       load_q(0);
       load_tile(v_s, &tm_v, &ctl.kv_full, hk, kt * kRows);
-      load_do(0);
     }
+    griddep_wait();  // do and the statistics come from prep
+    if (steps > 0) load_do(0);
   }
   if (warp == kWarpMma) {
     tmem_alloc(&ctl.tmem, 512);
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int which = cg >> 1, col = (cg & 1) * 64;
       const float mul = which ? scale : 1.f;
       __nv_bfloat16* dst = (which ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + col;
-      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * gridDim.x + blockIdx.x) * 2 + which) * kRows + r) * kD + col;
+      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * items + x) * 2 + which) * kRows + r) * kD + col;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t o[32];
@@ -557,6 +564,7 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4)
     window_join_kernel(const float* __restrict__ part, const WindowDev w, const DkvPlan plan,
                        int items, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
   constexpr int kSlices = kRows / kJoinRows;
+  griddep_wait();
   const int hk = blockIdx.y, b = blockIdx.z, slice = blockIdx.x % kSlices;
   const int which = blockIdx.x / kSlices & 1, s = blockIdx.x / (2 * kSlices);
   const int split_sinks = plan.sink_parts > 1 ? plan.sink_tiles : 0;
@@ -593,13 +601,12 @@ struct DqCtl {
 // Dynamic shared memory: Q, do, K ring, V ring.
 constexpr size_t kDqSmem = (2 + kDeep + kShort) * (size_t)kTileB;
 
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const WindowDev w, float sl, float scale, int n_pad,
-                     const float* __restrict__ nlse, const float* __restrict__ ndelta,
-                     __nv_bfloat16* __restrict__ dq, int* status) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, const CUtensorMap& tm_q,
+                                         const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const WindowDev& w, float sl,
+                                         float scale, int n_pad, const float* __restrict__ nlse,
+                                         const float* __restrict__ ndelta,
+                                         __nv_bfloat16* __restrict__ dq, int* status) {
   uint8_t* q_s = smem;
   uint8_t* do_s = q_s + kTileB;
   uint8_t* k_s = do_s + kTileB;
@@ -607,7 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   DqCtl& ctl = *reinterpret_cast<DqCtl*>(v_s + kShort * kTileB);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int qt = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / (w.heads / w.kv_heads);
   const int row0 = qt * kRows;
   const int len = window_length(w, b);
@@ -652,8 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_expect_tx(&ctl.q_full, 2 * kTileB);
       load_tile(q_s, &tm_q, &ctl.q_full, h, row0);
       load_k(0);
-      load_tile(do_s, &tm_do, &ctl.q_full, h, row0);
       load_v(0);
+      griddep_wait();  // do and the statistics come from prep
+      load_tile(do_s, &tm_do, &ctl.q_full, h, row0);
     }
   }
   if (warp == kWarpMma) {
@@ -765,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int all_end = pos1 - w.off - row0 < kRows - 1 ? 0 : min(window_end(w, w.off + row0), len);
     const int all_low = window_low(w, window_end(w, max(pos1, 0)));
     const size_t at = ((size_t)b * w.heads + h) * n_pad + row;  // row < n_pad
+    griddep_wait();
     const float nl = nlse[at], nd = ndelta[at];
     const bool live = nl != -INFINITY;
     const uint64_t sl2 = pk2(sl, sl), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
@@ -872,8 +880,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-constexpr size_t kSmemMax = 227 * 1024;
-static_assert(kDkvSmem + sizeof(DkvCtl) <= kSmemMax && kDqSmem + sizeof(DqCtl) <= kSmemMax, "shared memory");
+// ---------------------------------------------------------------- both
+constexpr size_t kDkvAll = kDkvSmem + sizeof(DkvCtl), kDqAll = kDqSmem + sizeof(DqCtl);
+constexpr size_t kGradSmem = kDkvAll > kDqAll ? kDkvAll : kDqAll;
+static_assert(kGradSmem <= 227 * 1024, "shared memory");
+
+// The dkv blocks, then the dq blocks, which fill the SMs of the last dkv wave.
+__global__ void __launch_bounds__(kThreads, 1)
+    window_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const WindowDev w, const DkvPlan plan, int items, int dkv_blocks, int q_tiles, float sl,
+                       float scale, int n_pad, const float* __restrict__ nlse,
+                       const float* __restrict__ ndelta, float* __restrict__ part,
+                       __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
+                       __nv_bfloat16* __restrict__ dv, int* status) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  griddep_launch_next();
+  int i = blockIdx.x;
+  if (i < dkv_blocks) {
+    const int x = i % items;
+    i /= items;
+    dkv_block(smem, x, items, i % w.kv_heads, i / w.kv_heads, tm_q, tm_do, tm_k, tm_v, w, plan, sl, scale,
+              n_pad, nlse, ndelta, part, dk, dv, status);
+  } else {
+    i -= dkv_blocks;
+    const int qt = q_tiles - 1 - i % q_tiles;  // the longest first
+    i /= q_tiles;
+    dq_block(smem, qt, i % w.heads, i / w.heads, tm_q, tm_do, tm_k, tm_v, w, sl, scale, n_pad, nlse, ndelta,
+             dq, status);
+  }
+}
 
 // A key tile is left whole while there are two CTAs for every SM; otherwise its
 // steps are cut so that there are, down to four steps each.  The sinks' tiles,
@@ -949,8 +985,7 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
       !make_tmap_bf16_3d(&tv, c.v, Ck, Nk, c.B, c.v_stride, Nk * c.v_stride, kRows))
     return fail(SANA_ERR_CUDA, "windowed anchor backward: cuTensorMapEncodeTiled failed");
   once_per_context(kAttrWindowBwd, [] {
-    cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDkvSmem + sizeof(DkvCtl)));
-    cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kDqSmem + sizeof(DqCtl)));
+    cudaFuncSetAttribute(window_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem);
   });
   using bf = __nv_bfloat16;
   const dim3 prep((unsigned)c.heads * (unsigned)(n_pad / kPrepRows), 1, c.B);
@@ -964,18 +999,19 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
   const float sl = c.scale * kLog2e;
   int* sw = status_word();
   const DkvPlan p = dkv_plan(c);
-  const int items = dkv_items(p);
-  window_dkv_kernel<<<dim3(items, c.kv_heads, c.B), kThreads, kDkvSmem + sizeof(DkvCtl), st>>>(
-      tq, td, tk, tv, w, p, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dk, (bf*)dv, sw);
-  if (sana_status e = check_launch("window_dkv_kernel")) return e;
+  const int items = dkv_items(p), q_tiles = n_pad / kRows;
+  const long long dkv_blocks = (long long)items * c.kv_heads * c.B, dq_blocks = (long long)q_tiles * c.heads * c.B;
+  if (dkv_blocks + dq_blocks > 0x7fffffffLL)
+    return fail(SANA_ERR_UNSUPPORTED, "windowed anchor backward: too many tiles (%lld)", dkv_blocks + dq_blocks);
+  launch_dependent(window_grad_kernel, dim3((unsigned)(dkv_blocks + dq_blocks)), dim3(kThreads), kGradSmem, st, tq, td,
+                   tk, tv, w, p, items, (int)dkv_blocks, q_tiles, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dq,
+                   (bf*)dk, (bf*)dv, sw);
+  if (sana_status e = check_launch("window_grad_kernel")) return e;
   const int split = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.win_parts > 1 ? p.tiles - p.sink_tiles : 0);
-  if (split) {
-    window_join_kernel<<<dim3(2 * split * (kRows / kJoinRows), c.kv_heads, c.B), kJoinRows * kD / 4, 0, st>>>(m.part, w, p, items, (bf*)dk, (bf*)dv);
-    if (sana_status e = check_launch("window_join_kernel")) return e;
-  }
-  window_dq_kernel<<<dim3((c.N + kRows - 1) / kRows, c.heads, c.B), kThreads, kDqSmem + sizeof(DqCtl), st>>>(
-      tq, td, tk, tv, w, sl, c.scale, n_pad, m.nlse, m.ndelta, (bf*)dq, sw);
-  return check_launch("window_dq_kernel");
+  if (!split) return SANA_OK;
+  launch_dependent(window_join_kernel, dim3(2 * split * (kRows / kJoinRows), c.kv_heads, c.B), dim3(kJoinRows * kD / 4),
+                   0, st, m.part, w, p, items, (bf*)dk, (bf*)dv);
+  return check_launch("window_join_kernel");
 }
 
 }  // namespace sana
