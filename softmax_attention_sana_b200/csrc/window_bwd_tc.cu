@@ -207,8 +207,8 @@ struct DkvCtl {
 // bytes from the 1024-aligned start), row statistics of each do stage.
 constexpr size_t kDkvSmem = (2 + kDeep + kShort) * (size_t)kTileB + kShort * 2 * kRows * sizeof(float);
 
-// Block (x, hk, b) of `items` x kv_heads x B.
-__device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int items, int hk, int b,
+// Share x of the key head hk and batch entry b, which have `slots` places in part.
+__device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int slots, int hk, int b,
                                           const CUtensorMap& tm_q, const CUtensorMap& tm_do,
                                           const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                           const WindowDev& w, const DkvPlan& plan, float sl,
@@ -514,7 +514,7 @@ __device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int items, int h
       const int which = cg >> 1, col = (cg & 1) * 64;
       const float mul = which ? scale : 1.f;
       __nv_bfloat16* dst = (which ? dk : dv) + (((size_t)b * w.N_keys + j) * w.kv_heads + hk) * kD + col;
-      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * items + x) * 2 + which) * kRows + r) * kD + col;
+      float* pdst = part + (((((size_t)b * w.kv_heads + hk) * slots + x) * 2 + which) * kRows + r) * kD + col;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t o[32];
@@ -562,7 +562,7 @@ __device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int items, int h
 constexpr int kJoinRows = 16;
 __global__ void __launch_bounds__(kJoinRows * kD / 4)
     window_join_kernel(const float* __restrict__ part, const WindowDev w, const DkvPlan plan,
-                       int items, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+                       int slots, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
   constexpr int kSlices = kRows / kJoinRows;
   griddep_wait();
   const int hk = blockIdx.y, b = blockIdx.z, slice = blockIdx.x % kSlices;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kJoinRows * kD / 4)
   const int i = slice * kJoinRows * (kD / 4) + threadIdx.x, j = kt * kRows + i / (kD / 4);
   if (j >= w.N_keys) return;
   const float4* p = reinterpret_cast<const float4*>(
-                        part + ((((size_t)b * w.kv_heads + hk) * items + item) * 2 + which) * kRows * kD) + i;
+                        part + ((((size_t)b * w.kv_heads + hk) * slots + item) * 2 + which) * kRows * kD) + i;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int k = 0; k < n; ++k) {
@@ -889,7 +889,7 @@ static_assert(kGradSmem <= 227 * 1024, "shared memory");
 __global__ void __launch_bounds__(kThreads, 1)
     window_grad_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const WindowDev w, const DkvPlan plan, int items, int dkv_blocks, int q_tiles, float sl,
+                       const WindowDev w, const DkvPlan plan, int items, int slots, int dkv_blocks, int q_tiles, float sl,
                        float scale, int n_pad, const float* __restrict__ nlse,
                        const float* __restrict__ ndelta, float* __restrict__ part,
                        __nv_bfloat16* __restrict__ dq, __nv_bfloat16* __restrict__ dk,
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (i < dkv_blocks) {
     const int x = i % items;
     i /= items;
-    dkv_block(smem, x, items, i % w.kv_heads, i / w.kv_heads, tm_q, tm_do, tm_k, tm_v, w, plan, sl, scale,
+    dkv_block(smem, x, slots, i % w.kv_heads, i / w.kv_heads, tm_q, tm_do, tm_k, tm_v, w, plan, sl, scale,
               n_pad, nlse, ndelta, part, dk, dv, status);
   } else {
     i -= dkv_blocks;
@@ -911,13 +911,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// A key tile is left whole while there are two CTAs for every SM; otherwise its
-// steps are cut so that there are, down to four steps each.  The sinks' tiles,
-// which all later queries see, are cut into shares as long as a window tile's, or
-// longer where that would make more of them than four for every SM.
+// A dkv block takes at most as many steps as would keep every SM busy equally long
+// (`even`: a dq block's step takes 7/10 of a dkv block's), so that the dq blocks can
+// fill what the dkv blocks leave, and a share at least kLeast.  The sinks' tiles,
+// which all later queries see, are cut to half of that.  Against cutting into two
+// blocks for every SM, down to 4 steps: 16000 rows, 1 head, window 1000, 54 against
+// 83 us; 2 x 4000 rows, 16 heads on 4, window 512, 216 against 265; 1023 rows, 8
+// heads on 1, no window, 40 against 34.  kLeast 4 or 6 against 8: 2000 rows, 4 heads,
+// no window, 52 against 42 us.
+constexpr long long kLeast = 8;
 DkvPlan dkv_plan(const WindowCall& c) {
   DkvPlan p{};
-  const long long group = c.heads / c.kv_heads;
+  const long long group = c.heads / c.kv_heads, columns = (long long)c.kv_heads * c.B;
   const long long q_tiles = (c.N + kRows - 1) / kRows;
   p.tiles = (c.N_keys + kRows - 1) / kRows;
   // query tiles that a key tile's window can reach
@@ -928,15 +933,16 @@ DkvPlan dkv_plan(const WindowCall& c) {
     p.sink_tiles = (c.sinks + kRows - 1) / kRows;
     if (p.sink_tiles > p.tiles) p.sink_tiles = p.tiles;
   }
-  const long long base = group * reach, columns = (long long)c.kv_heads * c.B;
-  const long long ctas = p.tiles * columns;
-  const long long parts = ctas >= 2 * kNumSMs ? 1 : (2 * kNumSMs + ctas - 1) / ctas;
-  long long chunk = (base + parts - 1) / parts;
-  if (chunk < 4) chunk = 4;
+  const long long base = group * reach, sink_steps = group * q_tiles;
+  // the last key tiles are seen from fewer query tiles
+  const long long pairs = columns * (group * (q_tiles * reach - reach * (reach - 1) / 2) + p.sink_tiles * sink_steps);
+  const long long even = (pairs * 17 / 10 + kNumSMs - 1) / kNumSMs;
+  long long chunk = even < kLeast ? kLeast : even;
+  if (chunk > base) chunk = base;
   p.win_chunk = (int)chunk;
   p.win_parts = (int)((base + chunk - 1) / chunk);
-  const long long sink_steps = group * q_tiles, most = sink_steps * p.sink_tiles * columns / (4 * kNumSMs) + 1;
-  if (chunk < most) chunk = most;
+  chunk = even / 2 < kLeast ? kLeast : even / 2;
+  if (chunk > sink_steps) chunk = sink_steps;
   p.sink_chunk = (int)chunk;
   p.sink_parts = (int)((sink_steps + chunk - 1) / chunk);
   return p;
@@ -944,8 +950,10 @@ DkvPlan dkv_plan(const WindowCall& c) {
 int dkv_items(const DkvPlan& p) {
   return p.sink_tiles * p.sink_parts + (p.tiles - p.sink_tiles) * p.win_parts;
 }
-bool dkv_split(const DkvPlan& p) {
-  return (p.sink_tiles && p.sink_parts > 1) || (p.tiles > p.sink_tiles && p.win_parts > 1);
+// Shares that are written out (the sinks' come first).
+int dkv_slots(const DkvPlan& p) {
+  if (p.win_parts > 1) return dkv_items(p);
+  return p.sink_parts > 1 ? p.sink_tiles * p.sink_parts : 0;
 }
 
 struct BwdWs {
@@ -962,7 +970,7 @@ BwdWs carve(const WindowCall& c, void* ws) {
   w.ndelta = cv.take<float>(rows);
   if (c.gate) w.d_o = cv.take<__nv_bfloat16>((size_t)c.B * c.N * c.heads * kD);
   const DkvPlan p = dkv_plan(c);
-  if (dkv_split(p)) w.part = cv.take<float>((size_t)c.B * c.kv_heads * dkv_items(p) * 2 * kRows * kD);
+  if (const int slots = dkv_slots(p)) w.part = cv.take<float>((size_t)c.B * c.kv_heads * slots * 2 * kRows * kD);
   w.bytes = align_up(cv.used, 256);
   return w;
 }
@@ -999,18 +1007,18 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
   const float sl = c.scale * kLog2e;
   int* sw = status_word();
   const DkvPlan p = dkv_plan(c);
-  const int items = dkv_items(p), q_tiles = n_pad / kRows;
+  const int items = dkv_items(p), slots = dkv_slots(p), q_tiles = n_pad / kRows;
   const long long dkv_blocks = (long long)items * c.kv_heads * c.B, dq_blocks = (long long)q_tiles * c.heads * c.B;
   if (dkv_blocks + dq_blocks > 0x7fffffffLL)
     return fail(SANA_ERR_UNSUPPORTED, "windowed anchor backward: too many tiles (%lld)", dkv_blocks + dq_blocks);
   launch_dependent(window_grad_kernel, dim3((unsigned)(dkv_blocks + dq_blocks)), dim3(kThreads), kGradSmem, st, tq, td,
-                   tk, tv, w, p, items, (int)dkv_blocks, q_tiles, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dq,
+                   tk, tv, w, p, items, slots, (int)dkv_blocks, q_tiles, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dq,
                    (bf*)dk, (bf*)dv, sw);
   if (sana_status e = check_launch("window_grad_kernel")) return e;
   const int split = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.win_parts > 1 ? p.tiles - p.sink_tiles : 0);
   if (!split) return SANA_OK;
   launch_dependent(window_join_kernel, dim3(2 * split * (kRows / kJoinRows), c.kv_heads, c.B), dim3(kJoinRows * kD / 4),
-                   0, st, m.part, w, p, items, (bf*)dk, (bf*)dv);
+                   0, st, m.part, w, p, slots, (bf*)dk, (bf*)dv);
   return check_launch("window_join_kernel");
 }
 

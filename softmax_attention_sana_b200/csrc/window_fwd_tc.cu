@@ -67,11 +67,16 @@ struct Form {
   static constexpr size_t kSmem = 1024 + 3 * kQ * (size_t)kTileB;
 };
 constexpr float kRescaleLog2 = 16.f;
-// Query tiles that see at most this many key tiles run one to a CTA.  16384 rows
-// of 16 heads, one against two: window 256 (4 tiles) 92 against 111 us, 1024 (10
-// tiles) 177 against 190 us, 4096 (34 tiles) 486 against 477 us; 32 heads on 8 key
-// heads with a gate: 210 against 244, 411 against 419, 1027 against 991 us.
-constexpr int kSingleReach = 10;
+// Query tiles that see at most this many key tiles run one to a CTA, and so does a
+// call whose tiles have an SM each.  One against two to a CTA, 16384 rows, 4 sinks:
+//   16 heads on 16: window 256 (5 tiles) 104 against 120 us, 512 (7) 142 against 154,
+//     1024 (11) 205 against 208, 2048 (19) 310 against 301
+//   16 heads on 4 (pairs of heads): 102 against 106, 131 against 131, 190 against
+//     182, 301 against 282
+//   32 heads on 8, gate: 242 against 233, 310 against 283, 418 against 383
+// no window, 4 heads on 1: 4096 rows (128 tiles) 66 against 70 us, 6000 (188) 98
+// against 96.
+constexpr int kSingleReach = 10, kSingleReachByHead = 6;
 // Of every 8 pairs of exponentials, on the FMA pipe.  Under the power cap, 32768 rows,
 // 32 heads, window 4096: none 2146 us, one 2130, two 2158 us.
 constexpr int kEmuPairs = 1;
@@ -572,12 +577,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
   }
 }
 
+// Two query heads of one key head make the better pair: both tiles see the same
+// keys (two tiles of rows leave each other idle at one end of the window: 16384
+// rows, 32 heads on 8, window 2048, 617 against 575 us).
+bool pairs_by_head(const WindowDev& w) { return w.heads / w.kv_heads % 2 == 0; }
+
 template <int kQ, bool kGate>
 void launch(const CUtensorMap* t, const WindowDev& w, int B, float sl, float* lse, cudaStream_t st) {
-  // Two query heads of one key head make the better pair: both tiles see the same
-  // keys (two tiles of rows leave each other idle at one end of the window: 16384
-  // rows, 32 heads on 8, window 2048, 617 against 575 us).
-  const int by_head = kQ == 2 && w.heads / w.kv_heads % 2 == 0;
+  const int by_head = kQ == 2 && pairs_by_head(w);
   const int rows = by_head ? kRows : kQ * kRows;
   const dim3 grid((w.N + rows - 1) / rows, by_head ? w.heads / 2 : w.heads, B);
   window_fwd_kernel<kQ, kGate><<<grid, Form<kQ>::kThreads, Form<kQ>::kSmem, st>>>(t[0], t[1], t[2], t[3], t[4], w,
@@ -613,7 +620,8 @@ sana_status window_fwd_run(const WindowCall& c, float* lse, void* out, cudaStrea
   const long long reach = c.window ? ((long long)c.window + c.block + 2 * kRows - 3) / kRows + 1 +
                                          (c.sinks + kRows - 1) / kRows
                                    : all;
-  const bool single = (reach < all ? reach : all) <= kSingleReach;
+  const bool single = (reach < all ? reach : all) <= (pairs_by_head(w) ? kSingleReachByHead : kSingleReach) ||
+                      ((long long)c.N + kRows - 1) / kRows * c.heads * c.B <= kNumSMs;
   if (single && c.gate) launch<1, true>(t, w, c.B, sl, lse, st);
   else if (single) launch<1, false>(t, w, c.B, sl, lse, st);
   else if (c.gate) launch<2, true>(t, w, c.B, sl, lse, st);

@@ -123,6 +123,8 @@ CASES = [  # B, N, Nk, heads, kv, window, sinks, block, lengths, gated, packed
     (2, 1100, 1100, 6, 2, 256, 4, 1, [1100, 900], True, True),
     (1, 2300, 2300, 1, 1, 512, 16, 1, None, False, False),
     (1, 2000, 2000, 8, 1, 64, 300, 1, None, False, True),          # three tiles of sinks, cut into shares
+    (1, 2500, 2500, 2, 1, 100, 1, 1, None, True, False),           # the sinks' tile cut, the others whole
+    (2, 5000, 5000, 1, 1, 4000, 2, 1, [5000, 3100], False, False),  # long key tiles beside short ones
     # more than ten key tiles to a query tile: two query tiles to a CTA
     (1, 1700, 1700, 2, 1, 0, 0, 1, None, True, False),
     (2, 1500, 1900, 4, 2, 1400, 9, 1, [1900, 1333], True, False),
