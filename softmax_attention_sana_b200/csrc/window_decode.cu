@@ -90,7 +90,9 @@ __device__ __forceinline__ KeyRuns key_runs(const DecodeDev& d, int len) {
   k.pos[1] = lo;
   k.slot[1] = at;
   k.rows[1] = upto;
-  if (at == s) {  // the window follows the sinks: one run
+  // the window follows the sinks' slots: one run, if the positions follow too or do
+  // not matter (a single query sees every listed key)
+  if (at == s && (lo == s || d.N == 1)) {
     k.rows[0] += upto;
     k.rows[1] = 0;
   }

@@ -244,6 +244,7 @@ DECODE = [  # B, N, heads, kv, capacity, window, sinks, gated, tokens already se
     (1, 5, 3, 3, 64, 8, 50, False, [1000]),
     (2, 7, 2, 1, 17, 300, 10, False, [40, 2]),            # the window is longer than the ring
     (5, 1, 40, 8, 257, 250, 6, True, [-1, 0, 1, 256, -7]),
+    (12, 3, 4, 2, 17, 9, 5, False, list(range(24, 36))),  # windows from every slot of the ring
 ]
 
 
