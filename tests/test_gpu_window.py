@@ -125,12 +125,20 @@ CASES = [  # B, N, Nk, heads, kv, window, sinks, block, lengths, gated, packed
     (1, 2000, 2000, 8, 1, 64, 300, 1, None, False, True),          # three tiles of sinks, cut into shares
     (1, 2500, 2500, 2, 1, 100, 1, 1, None, True, False),           # the sinks' tile cut, the others whole
     (2, 5000, 5000, 1, 1, 4000, 2, 1, [5000, 3100], False, False),  # long key tiles beside short ones
-    # more than ten key tiles to a query tile: two query tiles to a CTA
+    # more than ten key tiles to a query tile
     (1, 1700, 1700, 2, 1, 0, 0, 1, None, True, False),
     (2, 1500, 1900, 4, 2, 1400, 9, 1, [1900, 1333], True, False),
     (1, 1537, 1537, 2, 2, 1536, 100, 512, None, True, True),
     (3, 1665, 1665, 2, 1, 1500, 40, 1, [1665, 130, 0], False, False),
-    (2, 1600, 1600, 3, 1, 0, 0, 1, [1600, 700], True, True),       # an odd group: pairs of rows
+    (2, 1600, 1600, 3, 1, 0, 0, 1, [1600, 700], True, True),
+    # the same with more tiles than SMs
+    (1, 1700, 1700, 12, 6, 0, 0, 1, None, True, False),
+    (2, 1500, 1900, 8, 4, 1400, 9, 1, [1900, 1333], True, False),
+    (1, 1537, 1537, 12, 12, 1536, 100, 512, None, True, True),      # pairs of rows
+    (3, 1665, 1665, 4, 2, 1500, 40, 1, [1665, 130, 0], False, False),
+    (2, 1600, 1600, 6, 2, 0, 0, 1, [1600, 700], True, True),
+    (1, 1300, 1300, 16, 4, 700, 4, 1, None, False, True),
+    (2, 1111, 1500, 10, 5, 0, 0, 77, [1499, 0], False, False),
 ]
 
 
