@@ -23,7 +23,7 @@
 // 2 x 4001 tokens, 32 + 8 heads: 51 us for 246 MB (two tensors to load: 73%).  Bulk
 // copies into a ring in shared memory instead of loads to registers: 126 us.
 #include "f32x2.cuh"
-#include "pdl.cuh"
+#include "pdl_read.cuh"
 #include "rope_dev.cuh"
 #include "sana_common.cuh"
 #include "sana_internal.h"
@@ -325,6 +325,7 @@ template <class T, int LPR, bool HALF>
 __global__ void __launch_bounds__(32 * kWarpsBwd, 2)
     qk_norm_rope_bwd_kernel(const QkTensors a, const RotaryDev rt, float eps, float q_mul,
                             float* __restrict__ dw_part, int* status) {
+  griddep_launch_next();
   constexpr int D = LPR * 8, RPW = 32 / LPR, kU = kUnrollBwd<T>;
   __shared__ float red[kWarpsBwd][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -434,7 +435,8 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, 2)
 // dw[i] = sum over CTAs of part[cta][i]: 32 columns per CTA, each thread row
 // adds every 32nd partial, then the 32 rows are added in order.
 __global__ void __launch_bounds__(1024)
-    qk_dw_reduce_kernel(const float* __restrict__ part, int parts, int D, float* dwq, float* dwk) {
+    qk_dw_reduce_kernel(const float* part, int parts, int D, float* dwq, float* dwk) {
+  part = griddep_wait_for(part);
   __shared__ float red[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + c;
@@ -502,7 +504,7 @@ void launch_bwd(const QkTensors& a, const RotaryDev& rt, float eps, float q_mul,
   const int ctas = bwd_ctas((long long)a.B * a.N);
   if (ctas)  // no tokens: the sums over nothing below are zeros
     qk_norm_rope_bwd_kernel<T, LPR, HALF><<<ctas, 32 * kWarpsBwd, 0, st>>>(a, rt, eps, q_mul, ws, status_word());
-  qk_dw_reduce_kernel<<<(2 * LPR * 8 + 31) / 32, 1024, 0, st>>>(ws, ctas, LPR * 8, dwq, dwk);
+  launch_dependent(qk_dw_reduce_kernel, dim3((2 * LPR * 8 + 31) / 32), dim3(1024), 0, st, ws, ctas, LPR * 8, dwq, dwk);
 }
 
 // Calls f with the compile-time (type, lanes per row, layout) of the call.

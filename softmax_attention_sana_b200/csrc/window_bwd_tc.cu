@@ -41,7 +41,7 @@
 #include <cuda.h>
 
 #include "f32x2.cuh"
-#include "pdl.cuh"
+#include "pdl_read.cuh"
 #include "sana_internal.h"
 #include "tc_warp.cuh"
 #include "window.cuh"
@@ -561,10 +561,10 @@ __device__ __forceinline__ void dkv_block(uint8_t* smem, int x, int slots, int h
 // of a split key tile's dV or dK; key head; batch); thread = 4 columns of a row.
 constexpr int kJoinRows = 16;
 __global__ void __launch_bounds__(kJoinRows * kD / 4)
-    window_join_kernel(const float* __restrict__ part, const WindowDev w, const DkvPlan plan,
+    window_join_kernel(const float* part, const WindowDev w, const DkvPlan plan,
                        int slots, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
   constexpr int kSlices = kRows / kJoinRows;
-  griddep_wait();
+  part = griddep_wait_for(part);
   const int hk = blockIdx.y, b = blockIdx.z, slice = blockIdx.x % kSlices;
   const int which = blockIdx.x / kSlices & 1, s = blockIdx.x / (2 * kSlices);
   const int split_sinks = plan.sink_parts > 1 ? plan.sink_tiles : 0;
@@ -772,8 +772,7 @@ __device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, co
     const int all_end = pos1 - w.off - row0 < kRows - 1 ? 0 : min(window_end(w, w.off + row0), len);
     const int all_low = window_low(w, window_end(w, max(pos1, 0)));
     const size_t at = ((size_t)b * w.heads + h) * n_pad + row;  // row < n_pad
-    griddep_wait();
-    const float nl = nlse[at], nd = ndelta[at];
+    const float nl = griddep_wait_for(nlse)[at], nd = griddep_wait_for(ndelta)[at];
     const bool live = nl != -INFINITY;
     const uint64_t sl2 = pk2(sl, sl), nl2 = pk2(nl, nl), nd2 = pk2(nd, nd);
     bool ok = true;
