@@ -982,6 +982,11 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
                            void* dq, void* dk, void* dv, void* dg, void* ws, cudaStream_t st) {
   const BwdWs m = carve(c, ws);
   const int n_pad = pad_rows(c.N);
+  const DkvPlan p = dkv_plan(c);
+  const int items = dkv_items(p), slots = dkv_slots(p), q_tiles = n_pad / kRows;
+  const long long dkv_blocks = (long long)items * c.kv_heads * c.B, dq_blocks = (long long)q_tiles * c.heads * c.B;
+  if (dkv_blocks + dq_blocks > 0x7fffffffLL)
+    return fail(SANA_ERR_UNSUPPORTED, "windowed anchor backward: too many tiles (%lld)", dkv_blocks + dq_blocks);
   const WindowDev w{c.N, c.N_keys, c.N_keys - c.N, c.window, c.sinks, c.block, c.heads, c.kv_heads, c.lengths};
   const uint64_t N = c.N, Nk = c.N_keys, C = (uint64_t)c.heads * kD, Ck = (uint64_t)c.kv_heads * kD;
   const void* d_o = c.gate ? static_cast<const void*>(m.d_o) : dy;
@@ -1005,11 +1010,6 @@ sana_status window_bwd_run(const WindowCall& c, const void* y, const float* lse,
   if (sana_status e = check_launch("window_prep_kernel")) return e;
   const float sl = c.scale * kLog2e;
   int* sw = status_word();
-  const DkvPlan p = dkv_plan(c);
-  const int items = dkv_items(p), slots = dkv_slots(p), q_tiles = n_pad / kRows;
-  const long long dkv_blocks = (long long)items * c.kv_heads * c.B, dq_blocks = (long long)q_tiles * c.heads * c.B;
-  if (dkv_blocks + dq_blocks > 0x7fffffffLL)
-    return fail(SANA_ERR_UNSUPPORTED, "windowed anchor backward: too many tiles (%lld)", dkv_blocks + dq_blocks);
   launch_dependent(window_grad_kernel, dim3((unsigned)(dkv_blocks + dq_blocks)), dim3(kThreads), kGradSmem, st, tq, td,
                    tk, tv, w, p, items, slots, (int)dkv_blocks, q_tiles, sl, c.scale, n_pad, m.nlse, m.ndelta, m.part, (bf*)dq,
                    (bf*)dk, (bf*)dv, sw);

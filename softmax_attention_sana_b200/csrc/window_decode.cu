@@ -17,10 +17,11 @@
 //   P^T = 2^(sl S^T - m) in bf16, turned to (row, key) order by movmatrix
 //   O^T (128 d x 8 rows) += V^T P^T     A = V^T by ldmatrix.trans
 // Running maximum and sum in fp32; the warps of a CTA and then the CTAs of a
-// (sequence, key head) are joined in a fixed order: where they fit a cluster of up to
-// eight, in one another's shared memory, else through the workspace and a second kernel.  64 sequences of 8320 visible keys,
-// 16 query heads on 2 key heads: 88 us for 537 MB, 93% of the measured HBM rate; of
-// ragged lengths, 407 MB, 78 us (loads straight to registers, no ring: 93 us).
+// (sequence, key head) are joined in a fixed order: where they fit a cluster of up
+// to eight, in one another's shared memory, else through the workspace and a second
+// kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 88 us
+// for 537 MB, 93% of the measured HBM rate; of ragged lengths, 407 MB, 80 us (loads
+// straight to registers, no ring: 93 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
