@@ -10,8 +10,8 @@
 // The visible keys of a sequence are a few runs of slots (sinks, the window up
 // to the ring's end and from its start, the new tokens), cut into tiles of 64.  A
 // CTA takes a share of the tiles of one key head: a producer warp brings them in
-// by TMA (boxes of 16 rows, only those that hold visible keys) through a ring of
-// three stages, four warps take 16 keys of each.  The query rows of the key head
+// by TMA (whole tiles, or those boxes of 16 rows that hold visible keys) through a
+// ring of three stages, four warps take 16 keys of each.  The query rows of the key head
 // (N tokens x heads / kv_heads) form tiles of 8 (NT of them, 1 or 2, per CTA):
 //   S^T (16 keys x 8 rows) = K Q^T      A = K by ldmatrix
 //   P^T = 2^(sl S^T - m) in bf16, turned to (row, key) order by movmatrix
@@ -19,9 +19,9 @@
 // Running maximum and sum in fp32; the warps of a CTA and then the CTAs of a
 // (sequence, key head) are joined in a fixed order: where they fit a cluster of up
 // to eight, in one another's shared memory, else through the workspace and a second
-// kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 88 us
-// for 537 MB, 93% of the measured HBM rate; of ragged lengths, 407 MB, 80 us (loads
-// straight to registers, no ring: 93 us).
+// kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 87 us
+// for 545 MB, 95% of the measured HBM rate; of ragged lengths, 407 MB, 66 us (every
+// tile by boxes of 16 rows, one thread issuing 16 copies for each: 74 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -37,7 +37,7 @@ constexpr int kD = 128;
 constexpr int kWarps = 4;               // consumer warps; one more warp loads
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kTile = 64;               // keys of a tile: 16 for each warp
-constexpr int kBox = 16;                // rows of a TMA box
+constexpr int kBox = 16;                // rows of a TMA box of a tile that is not full
 constexpr int kStages = 3;
 constexpr int kHalf = kTile * 128;      // 64 columns of a tile's K or V, 8 KB
 constexpr int kStageB = 4 * kHalf;      // K and V of a tile, 32 KB
@@ -59,18 +59,42 @@ struct DecodeDev {
 struct KeyRuns {
   long long pos[4];  // positions may pass 2^31 by the N new tokens
   int slot[4], rows[4], tiles;
-  // Tile t: its run, and its first row there.
-  __device__ __forceinline__ void tile(int t, int& run, int& row) const {
-    run = 0;
+};
+// A walk over the tiles (every index is a constant, so that the runs stay in
+// registers).
+struct KeyTile {
+  long long pos;         // of its first key
+  int run, slot, left;   // keys of the run from here on
+  __device__ __forceinline__ void enter(const KeyRuns& k, int i) {
+    run = i;
+    pos = k.pos[i];
+    slot = k.slot[i];
+    left = k.rows[i];
+  }
+  __device__ __forceinline__ void seek(const KeyRuns& k, int t) {
+    enter(k, 0);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const int n = (rows[i] + kTile - 1) / kTile;
+      const int n = (k.rows[i] + kTile - 1) / kTile;
       if (run == i && t >= n) {
         t -= n;
-        run = i + 1;
+        enter(k, i + 1);
       }
     }
-    row = t * kTile;
+    step(t * kTile);
+  }
+  __device__ __forceinline__ void next(const KeyRuns& k) {
+    step(kTile);
+    if (left <= 0) {
+#pragma unroll
+      for (int i = 1; i < 4; ++i)
+        if (run < i && left <= 0) enter(k, i);
+    }
+  }
+  __device__ __forceinline__ void step(int n) {
+    pos += n;
+    slot += n;
+    left -= n;
   }
 };
 __device__ __forceinline__ KeyRuns key_runs(const DecodeDev& d, int len) {
@@ -162,6 +186,7 @@ __device__ __forceinline__ float load_cluster(uint32_t addr) {
 template <int NT, bool kJoined>
 __global__ void __launch_bounds__(kThreads, 2)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                          const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
                          const DecodeDev d, int* status) {
   constexpr int kRowsT = 8 * NT;
@@ -200,21 +225,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------ producer
     if (lane == 0) {
       int n = 0;
-      for (int t = 0; t < count; ++t) {
+      KeyTile at;
+      at.seek(keys, t0);
+      for (int t = 0; t < count; ++t, at.next(keys)) {
         const int st = t % kStages;
         if (t >= kStages && !mbar_wait(&ctl.empty[st], ((t / kStages) - 1) & 1, wc, 0xc1)) break;
-        int run, row;
-        keys.tile(t0 + t, run, row);
-        const int boxes = (min(kTile, keys.rows[run] - row) + kBox - 1) / kBox;
-        const CUtensorMap* mk = run == 3 ? &tm_kn : &tm_k;
-        const CUtensorMap* mv = run == 3 ? &tm_vn : &tm_v;
         uint8_t* dst = ring + st * kStageB;
-        mbar_arrive_expect_tx(&ctl.full[st], boxes * 4 * kBox * 128);
-        for (int x = 0; x < boxes; ++x)  // (rows past the cache's end read as zeros)
+        if (at.left >= kTile && at.run < 3) {
+          mbar_arrive_expect_tx(&ctl.full[st], kStageB);
           for (int hh = 0; hh < 2; ++hh) {
-            tma_load_3d(dst + hh * kHalf + x * kBox * 128, mk, &ctl.full[st], hk * kD + hh * 64, keys.slot[run] + row + x * kBox, b);
-            tma_load_3d(dst + (2 + hh) * kHalf + x * kBox * 128, mv, &ctl.full[st], hk * kD + hh * 64, keys.slot[run] + row + x * kBox, b);
+            tma_load_3d(dst + hh * kHalf, &tm_kt, &ctl.full[st], hk * kD + hh * 64, at.slot, b);
+            tma_load_3d(dst + (2 + hh) * kHalf, &tm_vt, &ctl.full[st], hk * kD + hh * 64, at.slot, b);
           }
+        } else {
+          const int boxes = (min(kTile, at.left) + kBox - 1) / kBox;
+          const CUtensorMap* mk = at.run == 3 ? &tm_kn : &tm_k;
+          const CUtensorMap* mv = at.run == 3 ? &tm_vn : &tm_v;
+          mbar_arrive_expect_tx(&ctl.full[st], boxes * 4 * kBox * 128);
+          for (int x = 0; x < boxes; ++x)  // (rows past the cache's end read as zeros)
+            for (int hh = 0; hh < 2; ++hh) {
+              tma_load_3d(dst + hh * kHalf + x * kBox * 128, mk, &ctl.full[st], hk * kD + hh * 64, at.slot + x * kBox, b);
+              tma_load_3d(dst + (2 + hh) * kHalf + x * kBox * 128, mv, &ctl.full[st], hk * kD + hh * 64, at.slot + x * kBox, b);
+            }
+        }
         ++n;
       }
       if (*wc.abort_flag)  // loads still in flight land before the CTA exits
@@ -274,37 +307,40 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int k_row = warp * 16 + (lane & 15), k_piece = lane >> 4;
   const int v_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3), v_piece = (lane >> 3) & 1;
   bool ok = true;
-  for (int u = 0; u < count; ++u) {
+  KeyTile at;
+  at.seek(keys, t0);
+  for (int u = 0; u < count; ++u, at.next(keys)) {
     const int st = u % kStages;
-    int run, row;
-    keys.tile(t0 + u, run, row);
     ok = __all_sync(0xffffffffu, mbar_wait(&ctl.full[st], (u / kStages) & 1, wc, 0xc2));
     if (!ok) break;
-    const int left = keys.rows[run] - row - warp * 16;  // keys of this warp
+    const int left = at.left - warp * 16;  // keys of this warp
     if (left > 0) {
       const uint32_t kb = smem_u32(ring + st * kStageB), vb = kb + 2 * kHalf;
-      float s[NT][4] = {};
+      float s[NT][4] = {}, s1[NT][4] = {};  // two chains of products, added below
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t ka[4];
         ldsm4(ka, kb + (j >> 2) * kHalf + sw128_off(k_row, (j & 3) * 2 + k_piece));
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816(s[t], ka, qr[t][j][0], qr[t][j][1]);
+        for (int t = 0; t < NT; ++t) mma16816(j & 1 ? s1[t] : s[t], ka, qr[t][j][0], qr[t][j][1]);
       }
       // s[t][e + 2 i]: key a + 8 i, query row 2c + e
       uint32_t p0[NT], p1[NT];
-      const long long first = keys.pos[run] + row + warp * 16;
+      const long long first = at.pos + warp * 16;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool in = a + 8 * i < left;
-          const long long p = first + a + 8 * i;
+        for (int i = 0; i < 4; ++i) s[t][i] = (s[t][i] + s1[t][i]) * d.sl;
+        if (!one || left < 16) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool sees = in && (one || (p <= qpos[t][e] &&
-                                             (d.window == 0 || p > qpos[t][e] - d.window || p < d.sinks)));
-            s[t][e + 2 * i] = sees ? s[t][e + 2 * i] * d.sl : -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            const long long p = first + a + 8 * i;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool sees = one || (p <= qpos[t][e] &&
+                                        (d.window == 0 || p > qpos[t][e] - d.window || p < d.sinks));
+              if (a + 8 * i >= left || !sees) s[t][e + 2 * i] = -INFINITY;
+            }
           }
         }
         float f[2][2];
@@ -513,9 +549,11 @@ sana_status window_decode_run(const DecodeCall& c, const void* q, const void* k_
                     (bf*)out, lengths, c.B, c.N, c.heads, c.kv_heads, c.capacity, c.window, c.sinks,
                     c.scale * kLog2e, p.row_tiles, (float*)ws};
   const uint64_t C = (uint64_t)c.kv_heads * kD, cap = c.capacity, N = c.N;
-  CUtensorMap tk, tv, tkn, tvn;
+  CUtensorMap tk, tv, tkt, tvt, tkn, tvn;
   if (!make_tmap_bf16_3d(&tk, k_cache, C, cap, c.B, C, cap * C, kBox) ||
       !make_tmap_bf16_3d(&tv, v_cache, C, cap, c.B, C, cap * C, kBox) ||
+      !make_tmap_bf16_3d(&tkt, k_cache, C, cap, c.B, C, cap * C, kTile) ||
+      !make_tmap_bf16_3d(&tvt, v_cache, C, cap, c.B, C, cap * C, kTile) ||
       !make_tmap_bf16_3d(&tkn, k_new, C, N, c.B, C, N * C, kBox) ||
       !make_tmap_bf16_3d(&tvn, v_new, C, N, c.B, C, N * C, kBox))
     return fail(SANA_ERR_CUDA, "windowed anchor step: cuTensorMapEncodeTiled failed");
@@ -540,12 +578,12 @@ sana_status window_decode_run(const DecodeCall& c, const void* q, const void* k_
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.nt == 1) cudaLaunchKernelEx(&cfg, window_decode_kernel<1, true>, tk, tv, tkn, tvn, d, sw);
-    else cudaLaunchKernelEx(&cfg, window_decode_kernel<2, true>, tk, tv, tkn, tvn, d, sw);
+    if (p.nt == 1) cudaLaunchKernelEx(&cfg, window_decode_kernel<1, true>, tk, tv, tkt, tvt, tkn, tvn, d, sw);
+    else cudaLaunchKernelEx(&cfg, window_decode_kernel<2, true>, tk, tv, tkt, tvt, tkn, tvn, d, sw);
     return check_launch("window_decode_kernel");
   }
-  if (p.nt == 1) window_decode_kernel<1, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
-  else window_decode_kernel<2, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkn, tvn, d, sw);
+  if (p.nt == 1) window_decode_kernel<1, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkt, tvt, tkn, tvn, d, sw);
+  else window_decode_kernel<2, false><<<grid, kThreads, kDecodeSmem, st>>>(tk, tv, tkt, tvt, tkn, tvn, d, sw);
   if (sana_status e = check_launch("window_decode_kernel")) return e;
   if (p.splits > 1) {
     launch_dependent(window_decode_join_kernel, dim3(c.heads / c.kv_heads * c.N, c.kv_heads, c.B), dim3(kD), 0, st,
