@@ -501,13 +501,15 @@ struct DecodePlan {
 };
 // Rows: one tile of 8 where they fit, else tiles of 16 (a second pass over the
 // keys costs more than the registers of 16 rows).  Splits: of those that the key
-// tiles allow, the one whose waves of CTAs (two fit on an SM) are soonest done,
-// with a CTA's start and end counted as two tiles and the second kernel as three.
-// Splits of one wave are clusters where they fit one (4 sequences of 1028 keys: 7.2
-// against 9.7 us; in several waves clusters wait for room: 91 against 79 us for 16
-// sequences, 24 key heads, 2052 keys).  64 sequences, 2 key heads,
-// 8320 keys: 2 splits in one wave 93 us, 4 in two 97 us, 9 in four 106 us; 16
-// sequences, 24 key heads, 2052 keys: 1 split in two waves 89 us, 3 in four 80 us.
+// tiles allow, the one whose waves of CTAs (two fit on an SM) are soonest done, with
+// a CTA's start and end counted as two tiles, the second kernel as one and each split
+// that it sums as a fifth.  Splits of one wave are clusters where they fit one; in
+// several waves clusters wait for room.  Measured, splits (j: in clusters):
+//   64 sequences of 8320 keys, 2 key heads: 1 88, 2 86, 2j 83, 4 87, 9 94 us
+//   4 of 1028, 8 key heads: 4j 7.3, 6j 7.5, 8j 6.5, 9 9.2
+//   2 of 8196, 2 key heads: 8j 13.7, 16 11.5, 32 11.1, 64 13.8
+//   1 of 4100, 8 key heads: 8j 8.7, 16 8.7, 32 10.1
+//   16 of 2052, 24 key heads: 1 70, 2 68, 3 68, 3j 73
 DecodePlan decode_plan(const DecodeCall& c) {
   DecodePlan p{};
   const int rows = c.heads / c.kv_heads * c.N;
@@ -516,13 +518,14 @@ DecodePlan decode_plan(const DecodeCall& c) {
   const long long items = (long long)c.B * c.kv_heads * p.row_tiles, slots = 2 * kNumSMs;
   long long keys = c.capacity;
   if (c.window && (long long)c.window + c.sinks + c.N < keys) keys = (long long)c.window + c.sinks + c.N;
-  const long long tiles = (keys + kTile - 1) / kTile;
+  const long long tiles = (keys + kTile - 1) / kTile + 2;  // (runs of keys end inside tiles)
   long long most = 4 * slots / items;  // four waves at most
   most = most < 1 ? 1 : most > tiles ? tiles : most;
   long long best = 0;
   for (long long s = 1; s <= most; ++s) {
     const bool joined = s <= kCluster && items * s <= slots;
-    const long long cost = (items * s + slots - 1) / slots * ((tiles + s - 1) / s + 2) + (joined ? 0 : 3);
+    const long long waves = (items * s + slots - 1) / slots;
+    const long long cost = 5 * waves * ((tiles + s - 1) / s + 2) + (s == 1 || joined ? 0 : 5 + s);
     if (best == 0 || cost < best) {
       best = cost;
       p.splits = (int)s;
