@@ -62,10 +62,13 @@ def test_workspace_sizes():
     stats = 2 * 64 * 1024 * 4
     assert plain == stats
     assert size(1, 1000, 1000, 64, 64, 128, gated=True) == stats + 1000 * 64 * 256
-    assert size(1, 1000, 1000, 64, 64, 128, sinks=4) > plain   # the sinks' tile is split
+    assert size(1, 1000, 1000, 64, 64, 128, sinks=4) == plain  # nor the sinks': 8 query tiles see it
+    share = 2 * 128 * 128 * 4                    # 32 query tiles: four shares of it, the others whole
+    assert size(1, 4000, 4000, 2, 2, 128, sinks=4) == 2 * 2 * 4096 * 4 + 2 * 4 * share
     assert size(1, 1000, 1000, 2, 2, 0) > size(1, 1000, 1000, 2, 2, 0, head_dim=64) == 0
     dec = _lib.window_anchor_decode_workspace_size
-    assert dec(1, 1, 8, 8, 4096, 0) == 8 * 32 * 8 * 130 * 4
+    assert dec(1, 1, 8, 8, 8192, 0) == 8 * 26 * 8 * 130 * 4
+    assert dec(1, 1, 8, 8, 1024, 0) == 0         # joined within a cluster
     assert dec(512, 1, 8, 8, 4096, 0) == 0
 
 
