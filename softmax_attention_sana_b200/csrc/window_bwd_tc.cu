@@ -933,8 +933,9 @@ DkvPlan dkv_plan(const WindowCall& c) {
     if (p.sink_tiles > p.tiles) p.sink_tiles = p.tiles;
   }
   const long long base = group * reach, sink_steps = group * q_tiles;
-  // the last key tiles are seen from fewer query tiles
-  const long long pairs = columns * (group * (q_tiles * reach - reach * (reach - 1) / 2) + p.sink_tiles * sink_steps);
+  // The last key tiles are seen from fewer query tiles.  (Tiles before the first
+  // window, which nobody sees, count too: their shares would take workspace.)
+  const long long pairs = columns * (group * (p.tiles * reach - reach * (reach - 1) / 2) + p.sink_tiles * sink_steps);
   const long long even = (pairs * 17 / 10 + kNumSMs - 1) / kNumSMs;
   long long chunk = even < kLeast ? kLeast : even;
   if (chunk > base) chunk = base;

@@ -65,6 +65,7 @@ def test_workspace_sizes():
     assert size(1, 1000, 1000, 64, 64, 128, sinks=4) == plain  # nor the sinks': 8 query tiles see it
     share = 2 * 128 * 128 * 4                    # 32 query tiles: four shares of it, the others whole
     assert size(1, 4000, 4000, 2, 2, 128, sinks=4) == 2 * 2 * 4096 * 4 + 2 * 4 * share
+    assert size(1, 128, 100000, 32, 2, 0) == 2 * 32 * 128 * 4  # many more keys than queries: none is split
     assert size(1, 1000, 1000, 2, 2, 0) > size(1, 1000, 1000, 2, 2, 0, head_dim=64) == 0
     dec = _lib.window_anchor_decode_workspace_size
     assert dec(1, 1, 8, 8, 8192, 0) == 8 * 26 * 8 * 130 * 4
