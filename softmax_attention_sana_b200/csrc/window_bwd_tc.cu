@@ -34,10 +34,11 @@
 // A product that overwrites what another reads waits for it by its barrier.
 // 16384 rows, 16 heads on 4 key heads, window 2048, 16 sinks: 815 us in all, 861 us
 // with dkv and dq as launches of their own (480 and 350 us: the dq blocks fill the
-// SMs that the last dkv wave leaves); 2 x 1023 rows, 8 heads, window 256: 40 against
-// 49 us.  Tensor pipe about 70% busy; in a long run the power cap holds it.  One warp
-// issues all products: with a second one for the dP chain dkv took 542 us (the
-// products then come in a worse order).
+// SMs that the last dkv wave leaves); 2 x 1023 rows, 8 heads, window 256, gate: 40
+// against 49 us, and 34 with the key tiles left whole (dkv_plan).  Tensor pipe about
+// 70% busy; in a long run the power cap holds it.  One warp issues all products: with
+// a second one for the dP chain dkv took 542 us (the products then come in a worse
+// order).
 #include <cuda.h>
 
 #include "f32x2.cuh"
