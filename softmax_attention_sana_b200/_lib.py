@@ -574,11 +574,16 @@ def _token_stride(t, name, width):
     seq, step, unit = t.stride()
     if C != width or (unit != 1 and C > 1):
         raise ValueError(f"{name} must be a CUDA tensor (B, N, {width}) with contiguous rows")
+    if B * N <= 1:
+        return width
     if N > 1:
         if B > 1 and seq != N * step:
             raise ValueError(f"{name}: sequences must follow each other at the tokens' stride")
-        return step if B else width
-    return seq if B > 1 and N else width
+    else:
+        step = seq
+    if step < width:  # (0, of an expanded tensor, would stand for the row's width)
+        raise ValueError(f"{name}: its tokens need rows of their own, {width} elements apart or more")
+    return step
 
 
 def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
