@@ -596,6 +596,7 @@ struct DqCtl {
   uint64_t k_full[kDeep], k_empty[kDeep];
   uint64_t v_full[kShort], v_empty[kShort];
   uint64_t s_full[2], dp_full, ds_full, dq_done;
+  uint64_t dq_last;  // the last product, and with it all before: completes once
   uint32_t tmem;
   int abort_flag;
 };
@@ -653,6 +654,7 @@ __device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, co
     mbar_init(&ctl.dp_full, 1);
     mbar_init(&ctl.ds_full, kSoft);
     mbar_init(&ctl.dq_done, 1);
+    mbar_init(&ctl.dq_last, 1);
     ctl.abort_flag = 0;
     mbar_fence_init();
     if (steps > 0) {  // the first loads run while the rest of the CTA sets up
@@ -751,7 +753,7 @@ __device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, co
         for (int kk = 0; kk < kRows / 16; ++kk)
           if (kk < ksteps) umma_ts_lead(lead, t_dq, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_advance(bm, kk * 2048),
                        idesc_g, (t | kk) != 0);
-        umma_commit_lead(lead, &ctl.dq_done);
+        umma_commit_lead(lead, t + 1 < steps ? &ctl.dq_done : &ctl.dq_last);
         umma_commit_lead(lead, &ctl.k_empty[t % kDeep]);
         if (t + 2 < steps) {
           if (!mbar_wait(&ctl.k_full[(t + 2) % kDeep], ((t + 2) / kDeep) & 1, wc, 0xb3) ||
@@ -842,11 +844,9 @@ __device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, co
       mbar_arrive(&ctl.ds_full);
     }
     // ---------------- epilogue: each quarter writes its 32 columns
-    // Nothing above waits for dQ(steps - 2): its phase is waited for first, or the
-    // parity of the last one would be taken for done while that one still runs.
-    // (dQ(steps - 3) ended before the last S was made.)
-    for (int t = max(steps - 2, 0); ok && t < steps; ++t)
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dq_done, t & 1, wc, 0xba));
+    // The last product has a barrier of its own: nothing here follows dq_done phase
+    // by phase, and both of its parities come round while these warps finish dS.
+    if (steps > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&ctl.dq_last, 0, wc, 0xba));
     if (ok) {
       tc_fence_after();
       __nv_bfloat16* dst = dq + (((size_t)b * w.N + row) * w.heads + h) * kD + cg * 32;
@@ -873,8 +873,7 @@ __device__ __forceinline__ void dq_block(uint8_t* smem, int qt, int h, int b, co
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
-    if (*wc.abort_flag)
-      for (int t = max(steps - 2, 0); t < steps; ++t) mbar_drain(&ctl.dq_done, t & 1);
+    if (*wc.abort_flag && steps > 0) mbar_drain(&ctl.dq_last, 0);  // MMAs in flight finish before TMEM is freed
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
