@@ -310,6 +310,17 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
         bool ok = true;
         for (int u = 0; ok && u < span.n; ++u) {
           if (!mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x95)) break;
+          const int key0 = span.tile(u) * kRows;
+          if (len < w.N_keys && key0 + kRows > len) {
+            // Padding rows of V meet P = 0: they are zeroed, whatever they hold, by this
+            // warp, the one that follows v_full phase by phase (the softmax warps skip
+            // tiles that their query tile does not see).
+            uint8_t* vt = v_s + (u % kStages) * kTileB;
+            for (int r = len - key0 + (lane >> 4); r < kRows; r += 2)
+              *reinterpret_cast<uint4*>(vt + (lane >> 3 & 1) * kHalf + sw128_off(r, lane & 7)) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
 #pragma unroll
           for (int i = 0; i < kQ; ++i) {
             if (!ok || !span.active(i, u)) continue;
@@ -357,15 +368,7 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     float m = -INFINITY, l = 0.f;  // row max reference and sum, base 2
     bool ok = true;
     int done = 0;
-    const bool pads = len < w.N_keys;  // V may hold padding rows, to be zeroed below
     for (int u = 0; ok && u < span.n; ++u) {
-      // Every V in turn, so that the parity waited for is always the next one.  (One
-      // query tile: S(u) was made after P V(u - 1), so V(u) is the next one anyway,
-      // and is waited for only where it is touched.)
-      if (kQ == 2 && pads && !__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
-        ok = false;
-        break;
-      }
       if (!span.active(qi, u)) continue;
       const int key0 = span.tile(u) * kRows;
       const int chunks = span.s[qi].width(span.tile(u), w.sinks) / 32;  // of 32 columns
@@ -450,21 +453,6 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       const uint64_t cfold = pk2(12582912.f - m_use, 12582912.f - m_use);
       const float s_lo = (m_use - 126.f) * inv_sl;
       uint64_t rs2 = pk2(0.f, 0.f);
-      if (pads && key0 + kRows > len) {
-        // padding rows of V meet P = 0: zero them, whatever they hold (both
-        // warpgroups write the same zeros before their own product reads V)
-        if (kQ == 1 && !__all_sync(0xffffffffu, mbar_wait(&ctl.v_full[u % kStages], (u / kStages) & 1, wc, 0x9d))) {
-          ok = false;
-          break;
-        }
-        uint8_t* vt = v_s + (u % kStages) * kTileB;
-        if (key0 + r >= len) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(vt + (c >> 3) * kHalf + sw128_off(r, c & 7)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
       if (kQ == 2 && done >= 1) {  // P of the tile before has been read
         if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x90))) {
           ok = false;

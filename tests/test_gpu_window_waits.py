@@ -45,3 +45,22 @@ def runs(B, N, Nk, heads, kv, window, sinks, block, lengths, gated, times, names
 ])
 def test_dq_is_read_after_its_last_product(N, Nk, window, sinks):
     runs(2, N, Nk, 6, 2, window, sinks, 1, None, False, 60, ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("B,N,Nk,heads,kv,window,sinks,block,lengths", [
+    # pairs of query tiles in different blocks: a run of key tiles that the first does not see
+    (2, 2600, 2600, 8, 8, 0, 0, 1280, [2500, 2600]),
+    (3, 2304, 2304, 8, 8, 1408, 3, 1152, [2304, 1300, 1153]),
+    # the first tile's window begins before the second's, sinks between
+    (2, 2000, 2300, 12, 12, 1500, 140, 1, [2299, 2050]),
+    # padding inside a tile that only the second tile sees; a sequence that ends in its first row
+    (4, 1600, 1600, 7, 7, 1500, 0, 1, [1409, 1408, 1537, 1]),
+    # two heads to a CTA
+    (2, 1700, 1700, 16, 4, 1500, 0, 1, [1601, 1700]),
+    # one query tile to a CTA
+    (3, 300, 300, 2, 1, 90, 2, 1, [300, 131, 128]),
+])
+def test_padded_values_are_cleared_by_whoever_reads_them(B, N, Nk, heads, kv, window, sinks, block, lengths):
+    """Values behind a sequence's end are infinite here (inputs() fills them in); the forward's result
+    alone is compared between runs, all of it with the formulas."""
+    runs(B, N, Nk, heads, kv, window, sinks, block, lengths, True, 25, ("y", "lse"))
