@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, 2)
       up2(gf, dot, t1);
       dot += t1;
       row_sum2<LPR>(ss, dot, lane);
-      const float r = rsqrtf(ss * (1.f / D) + eps);
+      // (rows past the last head: 1 / sqrt(0) of their zeros would reach dw for eps = 0)
+      const float r = hr < heads ? rsqrtf(ss * (1.f / D) + eps) : 0.f;
       const float k3 = -r * r * r * (dot * (1.f / D));
       const uint64_t r2 = pk2(r, r), k32 = pk2(k3, k3);
 #pragma unroll
