@@ -44,3 +44,13 @@ def test_no_eps(heads, kv, D, dtype, layout):
     dq, dk = make(2, B, N, heads, kv, D, dtype, False)
     wq = torch.linspace(0.5, 1.5, D).cuda()
     compare(q, k, dq, dk, wq, heads, kv, D, 0.0, layout)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [2.0 ** -46, 2.0 ** -30, 2.0 ** 30, 2.0 ** 46])
+def test_rows_far_from_one(size, dtype):
+    """Rows of 1e-14 to 1e14 with eps = 0: 1 / rms is a plain fp32 number, its cube is not."""
+    heads, kv, D = 4, 2, 128
+    q, k = (t * size for t in make(3, 2, 9, heads, kv, D, dtype, False))
+    dq, dk = make(4, 2, 9, heads, kv, D, dtype, False)
+    compare(q, k, dq, dk, torch.linspace(0.5, 1.5, D).cuda(), heads, kv, D, 0.0)
