@@ -159,12 +159,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 }
 
 // Output of one (row, column): o / l, gated.
-__device__ __forceinline__ void write_out(const DecodeDev& d, int b, int hk, int row, int col,
-                                          float o, float l) {
+__device__ __forceinline__ size_t out_at(const DecodeDev& d, int b, int hk, int row, int col) {
   const int group = d.heads / d.kv_heads;
   const int h = hk * group + row % group;
-  const size_t at = (((size_t)b * d.N + row / group) * d.heads + h) * kD + col;
-  float y = l > 0.f ? o / l : 0.f;
+  return (((size_t)b * d.N + row / group) * d.heads + h) * kD + col;
+}
+__device__ __forceinline__ void write_out(const DecodeDev& d, int b, int hk, int row, int col,
+                                          float o, float l) {
+  const size_t at = out_at(d, b, hk, row, col);
+  float y = o / l;  // (every row sees itself: l = 0 only where all its scores are -inf)
   if (d.gate) y *= sigmoid_fast(__bfloat162float(d.gate[at]));
   d.out[at] = __float2bfloat16(y);
 }
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (len < 0) {  // an empty batch entry
     if (split == 0)
       for (int i = threadIdx.x; i < min(kRowsT, rows - row0) * kD; i += kThreads)
-        write_out(d, b, hk, row0 + i / kD, i % kD, 0.f, 0.f);
+        d.out[out_at(d, b, hk, row0 + i / kD, i % kD)] = __float2bfloat16(0.f);
     return;
   }
   const KeyRuns keys = key_runs(d, len);

@@ -390,14 +390,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
         mbar_arrive(&ctl.s_taken);
       }
       auto chunk_max = [&](const uint32_t (&x)[32]) {  // two chains of 3-input max
-        float t = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-        float t2 = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
+        float t = max3_nan(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+        float t2 = max3_nan(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
 #pragma unroll
         for (int i = 6; i < 30; i += 4) {
-          t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          t2 = max3(t2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+          t = max3_nan(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          t2 = max3_nan(t2, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
         }
-        return fmaxf(max3(t, __uint_as_float(x[30]), __uint_as_float(x[31])), t2);
+        return max_nan(max3_nan(t, __uint_as_float(x[30]), __uint_as_float(x[31])), t2);
       };
       if (masked) {
 #pragma unroll
@@ -410,11 +410,11 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       }
       float top = -INFINITY;
       if (chunks == 4) {
-        top = fmaxf(fmaxf(chunk_max(sc[0]), chunk_max(sc[1])), fmaxf(chunk_max(sc[2]), chunk_max(sc[3])));
+        top = max3_nan(max_nan(chunk_max(sc[0]), chunk_max(sc[1])), chunk_max(sc[2]), chunk_max(sc[3]));
       } else {
 #pragma unroll
         for (int c = 0; c < 3; ++c)
-          if (c < chunks) top = fmaxf(top, chunk_max(sc[c]));
+          if (c < chunks) top = max_nan(top, chunk_max(sc[c]));
       }
       top *= sl;
       // The reference moves where the row's max passes it, on its first key or
@@ -491,7 +491,9 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       }
       float rs0, rs1;
       up2(rs2, rs0, rs1);
-      l += rs0 + rs1;
+      // a NaN or +inf score makes its row NaN (the exponentials on the FMA pipe would
+      // not show it)
+      l = top < INFINITY ? l + (rs0 + rs1) : NAN;
       ++done;
     }
     // ---------------- epilogue
@@ -505,7 +507,10 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     const uint8_t* gbuf = k_s + qi * kTileB;
     if (ok) {
       tc_fence_after();
-      const bool some = row_live && l > 0.f;
+      // A live row sees itself at least; where all its scores are -inf there is no
+      // softmax.  Dead rows get zeros.
+      const bool some = row_live;
+      if (m == -INFINITY) l = NAN;
       const float inv = some ? 1.f / l : 0.f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
