@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarpsBwd, 2)
       // (rows past the last head: 1 / sqrt(0) of their zeros would reach dw for eps = 0)
       const float r = hr < heads ? rsqrtf(ss * (1.f / D) + eps) : 0.f;
       // dot is of the size of 1 / r: taken in turn with it, r^3 leaves fp32 on neither side
-      const float k3 = -(dot * (1.f / D) * r) * r * r;
+      const float k3 = -(dot * (1.f / D) * r) * (r * r);
       const uint64_t r2 = pk2(r, r), k32 = pk2(k3, k3);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
