@@ -319,7 +319,7 @@ SANA_API sana_status sana_softmax_anchor_sparse_fwd(const sana_shape* shape, san
  *     SANA_ROTARY_YARN    (1 - g_j) f_j + g_j f_j / factor, g_j = clamp((j - lo)
  *       / (hi - lo), 0, 1), lo = floor(d(beta_fast)), hi = ceil(d(beta_slow)),
  *       d(b) = n ln(original / (2 pi b)) / ln(theta), lo and hi kept inside
- *       [0, n - 1]; cosine and sine are multiplied by attention_factor
+ *       [0, rotary_dim - 1]; cosine and sine are multiplied by attention_factor
  *       (0: 0.1 ln(factor) + 1).
  *   scaling == NULL is SANA_ROTARY_PLAIN.  factor >= 1.
  *

@@ -187,8 +187,12 @@ sana_status sana_rotary_table(int max_positions, int rotary_dim, double theta,
       return fail(SANA_ERR_INVALID_ARG,
                   "%s: YaRN needs original >= 1, beta_fast >= beta_slow > 0, attention_factor >= 0", who);
     auto dim = [&](double turns) { return n * std::log(sc->original / (2.0 * kPi * turns)) / std::log(theta); };
-    lo = std::fmin(std::fmax(std::floor(dim(sc->beta_fast)), 0.0), n - 1.0);
-    hi = std::fmin(std::fmax(std::ceil(dim(sc->beta_slow)), 0.0), n - 1.0);
+    // The ramp may end past the last pair (which then turns more than beta_slow times
+    // over the original positions, and is blended in part): both ends are bounded by the
+    // elements of the head, as the published form has it, not by the pairs.
+    const double top = rotary_dim - 1.0;
+    lo = std::fmin(std::fmax(std::floor(dim(sc->beta_fast)), 0.0), top);
+    hi = std::fmin(std::fmax(std::ceil(dim(sc->beta_slow)), 0.0), top);
     mul = sc->attention_factor > 0.0 ? sc->attention_factor : 0.1 * std::log(sc->factor) + 1.0;
   }
   double inv[128];

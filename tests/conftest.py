@@ -13,7 +13,19 @@ def pytest_configure(config):
     config.addinivalue_line("markers", "slow: full-size parity case (minutes of oracle time)")
 
 
+# Tests whose own expected value is wrong: they stay as they are, run, and have to fail.
+WRONG_VALUES = {
+    "test_gpu_rotary.py": ("-32-32-interleaved-('yarn', 2.0, 1048576)-",
+                           "expects YaRN's ramp to end at the last pair (15 of 16) where it ends at 21; "
+                           "the published bound is the rotary elements (test_gpu_yarn.py)"),
+}
+
+
 def pytest_collection_modifyitems(config, items):
+    for item in items:
+        part, reason = WRONG_VALUES.get(os.path.basename(str(item.path)), (None, None))
+        if part and part in item.name:
+            item.add_marker(pytest.mark.xfail(reason=reason, strict=True))
     # GPU tests need a CUDA device; they fail loudly (not skip) if the
     # extension is missing on a GPU machine, but are skipped on CPU-only hosts.
     try:
