@@ -82,31 +82,6 @@ constexpr int kSingleReach = 10, kSingleReachByHead = 6;
 constexpr int kEmuPairs = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// 2^(sl * s - m) for two scores on the FMA pipe, m an integer below 2^22 in
-// magnitude.  c = 1.5 * 2^23 - m: t = sl s + c holds n = round(sl s - m) in its
-// low mantissa bits, f = sl s - (t - c) lies in [-1/2, 1/2], 2^f is a cubic
-// fitted for it (7.5e-5 relative, far below the bf16 step of P), and n is added
-// to the exponent field.  Scores below s_lo = (m - 126) / sl count as s_lo:
-// 2^-126 instead of less, nothing beside the row's largest term.
-__device__ __forceinline__ void exp2_scaled2(float s0, float s1, float s_lo, uint64_t sl, uint64_t c,
-                                             float& y0, float& y1) {
-  const uint64_t s = pk2(fmaxf(s0, s_lo), fmaxf(s1, s_lo));
-  const uint64_t t = fma2(s, sl, c);
-  const uint64_t d = sub2(c, t);  // -(n + m)
-  const uint64_t f = fma2(s, sl, d);
-  uint64_t p = fma2(pk2(0.055170517f, 0.055170517f), f, pk2(0.24260856f, 0.24260856f));
-  p = fma2(p, f, pk2(0.69326097f, 0.69326097f));
-  p = fma2(p, f, pk2(0.99992824f, 0.99992824f));
-  float t0, t1, p0, p1;
-  up2(t, t0, t1);
-  up2(p, p0, p1);
-  uint32_t r0, r1;
-  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r0) : "r"(__float_as_uint(t0)), "r"(__float_as_uint(p0)));
-  asm("mad.lo.u32 %0, %1, 8388608, %2;" : "=r"(r1) : "r"(__float_as_uint(t1)), "r"(__float_as_uint(p1)));
-  y0 = __uint_as_float(r0);
-  y1 = __uint_as_float(r1);
-}
-
 template <int kQ>
 struct WinCtl {
   uint64_t q_full, g_full;
@@ -364,7 +339,6 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
     const int all_end = min(window_end(w, pos0), len);       // every live row sees below it
     const int all_low = window_low(w, window_end(w, max(pos1, 0)));  // every live row sees from it on
     const uint64_t sl2 = pk2(sl, sl);
-    const float inv_sl = 1.f / sl;
     float m = -INFINITY, l = 0.f;  // row max reference and sum, base 2
     bool ok = true;
     int done = 0;
@@ -418,10 +392,9 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       }
       top *= sl;
       // The reference moves where the row's max passes it, on its first key or
-      // by more than 2^16.  It is rounded up to an integer for the folded
-      // constants of exp2_scaled2.  A row that has seen no key yet keeps -inf
-      // and works against 0: its terms are 2^-inf (or 2^-126, dropped by the
-      // factor 0 when its first key comes).
+      // by more than 2^16.  It is rounded up to an integer: rescaling is then exact.
+      // A row that has seen no key yet keeps -inf and works against 0: its terms are
+      // 2^-inf (or 2^-126, dropped by the factor 0 when its first key comes).
       const bool grow = top > m + kRescaleLog2;
       if (__any_sync(0xffffffffu, grow)) {
         const float m_next = grow ? ceilf(top) : m;
@@ -450,8 +423,6 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
       }
       const float m_use = m == -INFINITY ? 0.f : m;
       const uint64_t neg_m = pk2(-m_use, -m_use);
-      const uint64_t cfold = pk2(12582912.f - m_use, 12582912.f - m_use);
-      const float s_lo = (m_use - 126.f) * inv_sl;
       uint64_t rs2 = pk2(0.f, 0.f);
       if (kQ == 2 && done >= 1) {  // P of the tile before has been read
         if (!__all_sync(0xffffffffu, mbar_wait(&ctl.pv_done[qi], (done - 1) & 1, wc, 0x90))) {
@@ -467,14 +438,14 @@ __global__ void __launch_bounds__(Form<kQ>::kThreads, 3 - kQ)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const float s0 = __uint_as_float(sc[c][i]), s1 = __uint_as_float(sc[c][i + 1]);
+            const uint64_t x = fma2(pk2(s0, s1), sl2, neg_m);
             float p0, p1;
             if (((i >> 1) & 7) >= 8 - kEmuPairs) {
-              exp2_scaled2(s0, s1, s_lo, sl2, cfold, p0, p1);
+              exp2_pair(x, p0, p1);
             } else {
-              float x0, x1;
-              up2(fma2(pk2(s0, s1), sl2, neg_m), x0, x1);
-              p0 = ex2(x0);
-              p1 = ex2(x1);
+              up2(x, p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
             }
             rs2 = add2(rs2, pk2(p0, p1));
             pk[i / 2] = f2_to_bf2(p0, p1);
