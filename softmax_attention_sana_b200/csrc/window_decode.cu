@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = (s[t][i] + s1[t][i]) * d.sl;
+        for (int i = 0; i < 4; ++i) s[t][i] += s1[t][i];
         if (!one || left < 16) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float top = fmaxf(s[t][e], s[t][e + 2]);
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-          const float now = fmaxf(mx[t][e], top);
+          const float now = fmaxf(mx[t][e], top * d.sl);
           const float ref = now == -INFINITY ? 0.f : now;
           const float corr = ex2(mx[t][e] - ref);  // 1 where the maximum stayed, 0 before the first key
           if (__any_sync(0xffffffffu, now != mx[t][e])) {
@@ -363,8 +363,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
           }
           mx[t][e] = now;
-          f[e][0] = ex2(s[t][e] - ref);
-          f[e][1] = ex2(s[t][e + 2] - ref);
+          // (scaled and referred in one rounding: of large scores only the differences count)
+          f[e][0] = ex2(fmaf(s[t][e], d.sl, -ref));
+          f[e][1] = ex2(fmaf(s[t][e + 2], d.sl, -ref));
           sum[t][e] = sum[t][e] * corr + (f[e][0] + f[e][1]);
         }
         p0[t] = transpose8(f2_to_bf2(f[0][0], f[1][0]));

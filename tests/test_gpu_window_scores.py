@@ -39,3 +39,17 @@ def test_a_large_common_score_cancels(N, heads, kv, window, block, c, scale, sig
     check("y", y, ref)
     want = ref["lse"][0]
     assert ((lse.double() - want).abs() <= 4 * 2.0 ** -24 * want.abs() + 2e-4).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("c,scale", [(22, 0.5), (26, 0.0), (30, 2.0 ** -9)])
+def test_the_step_too(c, scale, sign):
+    N, heads, kv = 70, 4, 2
+    q, k, v, g, dy = rows(c, N, heads, kv, c, sign)
+    ref = reference(q, k, v, g, dy, heads, kv, 0, 0, 1, None, scale or 1 / math.sqrt(D))
+    caches = [torch.zeros(1, 80, kv * D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    out = [sana.window_anchor_decode(*(t[:, i:i + 1].contiguous() for t in (q, k, v, g)), *caches,
+                                     torch.full((1,), i, dtype=torch.int32, device="cuda"), heads, kv, 0, scale=scale)
+           for i in range(N)]
+    sana.sync_status()
+    check("y", torch.cat(out, dim=1), ref)
