@@ -506,6 +506,13 @@ _LAYOUTS = {"interleaved": ROTARY_INTERLEAVED, "half": ROTARY_HALF}
 _SCALINGS = {"linear": 1, "ntk": 2, "yarn": 3}
 
 
+def _c_int(*values):
+    """Refuses what ctypes would cut to 32 bits."""
+    for v in values:
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{v} does not fit a C int")
+
+
 class Rotary:
     """Device table of rotary (cos, sin) for positions [0, max_positions): rotary_dim elements of a
     head are turned (the rest pass through), paired "interleaved" (2j, 2j + 1) or "half" (j, j +
@@ -523,7 +530,9 @@ class Rotary:
                     (kind == "yarn" and len(rest) < 2):
                 raise ValueError(f"bad rotary scaling {scaling!r}")
             factor, original, fast, slow, att = (list(rest) + [0, 32.0, 1.0, 0.0][len(rest) - 1:])
+            _c_int(original)
             sc = RotaryScaling(_SCALINGS[kind], factor, original, fast, slow, att)
+        _c_int(max_positions, rotary_dim)
         self.max_positions, self.rotary_dim, self.layout = max_positions, rotary_dim, layout
         self.table = torch.empty(max(max_positions, 1), max(rotary_dim // 2, 1), 2,
                                  dtype=torch.float32, device=device)
@@ -600,6 +609,7 @@ def _qk_call(q, k, rotary, heads, kv_heads, positions, offset, grid):
         Bk, Nk, _ = k.shape
         if k.dtype is not q.dtype or Bk != B or Nk != N:
             raise ValueError("q and k must have one dtype and the same (B, N)")
+    _c_int(offset, *(grid or ()))
     s = QkShape(B, N, heads, kv_heads, D, _token_stride(q, "q", C), k_stride)
     at_positions = None
     if positions is not None:
@@ -671,6 +681,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, rotary, heads, kv_heads, positions=No
 
 
 def qk_norm_rope_bwd_workspace_size(B, N, head_dim) -> int:
+    _c_int(B, N, head_dim)
     s = QkShape(B, N, 1, 0, head_dim, 0, 0)
     return lib.sana_qk_norm_rope_bwd_workspace_size(ctypes.byref(s))
 
@@ -723,6 +734,7 @@ def _window_shape(q, k, v, gate, heads, kv_heads, window, sinks, block, lengths,
         if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
             raise ValueError("lengths must be a contiguous int32 tensor (B,)")
         at_lengths = lengths.data_ptr()
+    _c_int(window, sinks, block)
     _same_device(q, k, v, gate, lengths)
     return WindowShape(B, N, k.shape[1], heads, kv_heads, D, *strides, window, sinks, block,
                        at_lengths, scale)
@@ -751,6 +763,7 @@ def window_anchor_fwd(q, k, v, gate, heads, kv_heads, window, sinks=0, block=1, 
 
 def window_anchor_bwd_workspace_size(B, N, N_keys, heads, kv_heads, window, sinks=0, block=1,
                                      gated=False, head_dim=128) -> int:
+    _c_int(B, N, N_keys, heads, kv_heads, window, sinks, block, head_dim)
     s = WindowShape(B, N, N_keys, heads, kv_heads, head_dim, 0, 0, 0, 0, window, sinks, block, None, 0.0)
     return lib.sana_window_anchor_bwd_workspace_size(ctypes.byref(s), int(bool(gated)))
 
@@ -780,6 +793,7 @@ def window_anchor_bwd(q, k, v, gate, out, lse, dy, heads, kv_heads, window, sink
 
 def window_anchor_decode_workspace_size(B, N, heads, kv_heads, capacity, window, sinks=0,
                                         head_dim=128) -> int:
+    _c_int(B, N, heads, kv_heads, capacity, window, sinks, head_dim)
     s = WindowDecodeShape(B, N, heads, kv_heads, head_dim, capacity, window, sinks, 0.0)
     return lib.sana_window_anchor_decode_workspace_size(ctypes.byref(s))
 
@@ -809,6 +823,7 @@ def window_anchor_decode(q, k, v, gate, k_cache, v_cache, lengths, heads, kv_hea
         raise ValueError("the caches must be (B, capacity, kv_heads * head_dim)")
     if lengths.dtype is not torch.int32 or lengths.shape != (B,) or not lengths.is_contiguous():
         raise ValueError("lengths must be a contiguous int32 tensor (B,)")
+    _c_int(window, sinks)
     _same_device(q, k, v, gate, k_cache, v_cache, lengths)
     s = WindowDecodeShape(B, N, heads, kv_heads, D, capacity, window, sinks, scale)
     out = _out_like(out, "out", q, C)
