@@ -540,6 +540,8 @@ class Rotary:
             check(lib.sana_rotary_table(max_positions, rotary_dim, theta,
                                         None if sc is None else ctypes.byref(sc), _ptr(self.table),
                                         _stream()))
+            if not torch.cuda.is_current_stream_capturing():  # any stream may use the table from here on
+                torch.cuda.current_stream().synchronize()
         self.struct = RotaryStruct(self.table.data_ptr(), max_positions, rotary_dim, _LAYOUTS[layout])
         self.pointer = ctypes.pointer(self.struct)
 
