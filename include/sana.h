@@ -437,7 +437,8 @@ SANA_API sana_status sana_qk_norm_rope_bwd(const sana_qk_shape* shape, sana_dtyp
  *   that the shape fixes.  Workspace: sana_window_anchor_bwd_workspace_size()
  *   bytes (gated != 0 for a call with a gate), 256-byte aligned.
  * Accuracy: scores and sums in fp32; P, dS and sigmoid(G) dy are rounded to
- * bf16 as operands of the next product.  A NaN or +inf among the scores that a
+ * bf16 as operands of the next product; the backward takes P from lse, which
+ * adds a relative 2^-23 |lse|.  A NaN or +inf among the scores that a
  * row sees makes its output and lse NaN, and so do scores that are all -inf.  A
  * non-finite value in a real token's row can also reach the rows that share a
  * 128-key tile with it.

@@ -19,9 +19,11 @@
 // the angles.  A lane holds 8 consecutive elements of a row (16-byte accesses) and
 // a row sits in head_dim / 8 neighbouring lanes (the partner in the half layout
 // is a shuffle away), several row groups in flight.  480p grid (32760 tokens, 16 + 16
-// heads of 128, bf16): 87 us for 537 MB, 94% of the measured HBM rate; gradient of
-// 2 x 4001 tokens, 32 + 8 heads: 51 us for 246 MB (two tensors to load: 73%).  Bulk
-// copies into a ring in shared memory instead of loads to registers: 126 us.
+// heads of 128, bf16): 85 us for 537 MB, 96% of the measured HBM rate; 2 x 8192 tokens,
+// 32 + 8 heads (335 MB) from flushed caches: 62 us interleaved, 68 half (which spills,
+// kResident), the rotation alone 61 and 62; their gradient (503 MB) 100 and 106 us (two
+// tensors to load: 77 and 72%).  Bulk copies into a ring in shared memory instead of
+// loads to registers, on the 480p grid: 126 us.
 #include "f32x2.cuh"
 #include "pdl_read.cuh"
 #include "rope_dev.cuh"
@@ -38,7 +40,9 @@ constexpr int kUnroll = 4;     // row groups a warp has in flight (forward)
 template <class T>
 constexpr int kUnrollBwd = sizeof(T) == 2 ? 4 : 2;
 // CTAs on an SM that the forward's registers are held to (bf16: 480p grid, 16 heads
-// of 128: 87 us against 91 us unheld; fp32 rows need the registers).
+// of 128, interleaved: 87 us against 91 us unheld; fp32 rows need the registers).  Held
+// so, every bf16 form of the half layout spills (156 to 252 bytes of stores a thread);
+// a bound of its own has not been measured.
 template <class T>
 constexpr int kResident = sizeof(T) == 2 ? 7 : 4;
 

@@ -19,9 +19,10 @@
 // Running maximum and sum in fp32; the warps of a CTA and then the CTAs of a
 // (sequence, key head) are joined in a fixed order: where they fit a cluster of up
 // to eight, in one another's shared memory, else through the workspace and a second
-// kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 87 us
-// for 545 MB, 95% of the measured HBM rate; of ragged lengths, 407 MB, 66 us (every
-// tile by boxes of 16 rows, one thread issuing 16 copies for each: 74 us).
+// kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 84 us
+// for 545 MB, 98% of the measured HBM rate (two splits in a cluster); of ragged lengths,
+// 407 MB, 65 us (an earlier form that brought every tile in by boxes of 16 rows, one
+// thread issuing 16 copies for each, took 74 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -508,12 +509,13 @@ struct DecodePlan {
 // tiles allow, the one whose waves of CTAs (two fit on an SM) are soonest done, with
 // a CTA's start and end counted as two tiles, the second kernel as one and each split
 // that it sums as a fifth.  Splits of one wave are clusters where they fit one; in
-// several waves clusters wait for room.  Measured, splits (j: in clusters):
-//   64 sequences of 8320 keys, 2 key heads: 1 88, 2 86, 2j 83, 4 87, 9 94 us
-//   4 of 1028, 8 key heads: 4j 7.3, 6j 7.5, 8j 6.5, 9 9.2
-//   2 of 8196, 2 key heads: 8j 13.7, 16 11.5, 32 11.1, 64 13.8
-//   1 of 4100, 8 key heads: 8j 8.7, 16 8.7, 32 10.1
-//   16 of 2052, 24 key heads: 1 70, 2 68, 3 68, 3j 73
+// several waves clusters wait for room.  Measured in captured runs over caches beyond
+// L2, splits (j: in clusters):
+//   64 sequences of 8320 keys, 2 key heads: 1 90, 2 88, 2j 84, 4 88, 9 94 us
+//   4 of 1028, 8 key heads: 4j 8.5, 6j 8.7, 8j 8.7, 9 11.1
+//   2 of 8196, 2 key heads: 8j 15.4, 16 12.8, 32 13.0, 64 15.9
+//   1 of 4100, 8 key heads: 8j 10.0, 16 10.6, 32 12.3 (17, taken here: 11.0)
+//   16 of 2052, 24 key heads: 1 71, 2 69, 3 69, 3j 74
 DecodePlan decode_plan(const DecodeCall& c) {
   DecodePlan p{};
   const int rows = c.heads / c.kv_heads * c.N;

@@ -35,9 +35,14 @@
 // against 2095 us.)  One query tile: S with P over its first half, and O, 256
 // columns.
 //
-// Bound by the tensor core (4 * 128 flops per pair and head) and, in a long run,
-// by the power that it and the exponentials draw together: 16384 x 16 rows, window
-// 4096, 1.2 PFLOP/s; 32768 x 32 rows at the 1 kW cap (1.64 GHz) 985 TFLOP/s.
+// The products (4 * 128 flops per pair and head) fill a little over half of the
+// time: 8192 rows, 32 heads on 8, window 4096: 351 k of a launch's 671 k cycles, tensor
+// pipe 58% active.  The softmax warps are longer at a step of two tiles than its
+// products (about 3350 cycles against 2048, in a trace of an earlier form), and some
+// seven CTAs follow one another on an SM, each with its start and end in the open.
+// In a long run the power cap takes the clock down as well.  32768 rows, 32 heads on 8,
+// window 4096: 1794 us for single calls (1.15 PFLOP/s), 2090 us in a run of 2 s (at 1 kW,
+// 986 TFLOP/s).
 #include <cuda.h>
 
 #include "f32x2.cuh"
@@ -78,7 +83,8 @@ constexpr float kRescaleLog2 = 16.f;
 // against 96.
 constexpr int kSingleReach = 10, kSingleReachByHead = 6;
 // Of every 8 pairs of exponentials, on the FMA pipe.  Under the power cap, 32768 rows,
-// 32 heads, window 4096: none 2146 us, one 2130, two 2158 us.
+// 32 heads on 8, window 4096: none 2110 us, one 2090, two 2097 us; 18720 rows, 16 heads,
+// blocks of 4680, gate: 1437, 1433, 1462 us.
 constexpr int kEmuPairs = 1;
 constexpr float kLn2 = 0.6931471805599453f;
 
