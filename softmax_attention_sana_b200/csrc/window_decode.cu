@@ -20,9 +20,9 @@
 // (sequence, key head) are joined in a fixed order: where they fit a cluster of up
 // to eight, in one another's shared memory, else through the workspace and a second
 // kernel.  64 sequences of 8320 visible keys, 16 query heads on 2 key heads: 84 us
-// for 545 MB, 98% of the measured HBM rate (two splits in a cluster); of ragged lengths,
-// 407 MB, 65 us (an earlier form that brought every tile in by boxes of 16 rows, one
-// thread issuing 16 copies for each, took 74 us).
+// for 545 MB, 98% of the measured HBM rate, in a run of calls (two splits in a cluster;
+// 88 us alone); of ragged lengths, 407 MB, 65 us (an earlier form that brought every tile
+// in by boxes of 16 rows, one thread issuing 16 copies for each, took 74 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

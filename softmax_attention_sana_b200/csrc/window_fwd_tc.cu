@@ -36,7 +36,7 @@
 // columns.
 //
 // The products (4 * 128 flops per pair and head) fill a little over half of the
-// time: 8192 rows, 32 heads on 8, window 4096: 351 k of a launch's 671 k cycles, tensor
+// time: 8192 rows, 32 heads on 8, window 4096: 351 k of a launch's 670 k cycles, tensor
 // pipe 58% active.  The softmax warps are longer at a step of two tiles than its
 // products (about 3350 cycles against 2048, in a trace of an earlier form), and some
 // seven CTAs follow one another on an SM, each with its start and end in the open.
