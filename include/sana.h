@@ -438,10 +438,11 @@ SANA_API sana_status sana_qk_norm_rope_bwd(const sana_qk_shape* shape, sana_dtyp
  *   bytes (gated != 0 for a call with a gate), 256-byte aligned.
  * Accuracy: scores and sums in fp32; P, dS and sigmoid(G) dy are rounded to
  * bf16 as operands of the next product; the backward takes P from lse, which
- * adds a relative 2^-23 |lse|.  A NaN or +inf among the scores that a
- * row sees makes its output and lse NaN, and so do scores that are all -inf.  A
- * non-finite value in a real token's row can also reach the rows that share a
- * 128-key tile with it.
+ * adds a relative 2^-23 |lse|.  The forward's sums hold weights of up to 2^16
+ * before the last division: |V| times the visible keys must stay below 2^111.
+ * A NaN or +inf among the scores that a row sees makes its output and lse NaN,
+ * and so do scores that are all -inf.  A non-finite value in a real token's row
+ * can also reach the rows that share a 128-key tile with it.
  *
  * sana_window_anchor_decode: the N newest tokens (N small, usually 1) of every
  *   sequence over a cache of sinks and window that does not grow.  q (B, N,
